@@ -1,0 +1,648 @@
+// Norms before and after a block with gate and residual scale (block_norm.h).
+//
+// Forward: one workgroup per row at a time, the whole row in registers: one
+// read of x and y, one write of x' and u.  Two joins over the workgroup (the
+// mean square of y, then of x', which needs the first), a third for the
+// largest |u| when u is quantised.
+//
+// Backward: a workgroup walks a run of consecutive rows and keeps the sums
+// for dw_post, dw_pre and dgate of its columns in registers; two joins per
+// row (mean squares of x' and y and the product a.x' together, then b.y).
+// The partial sums go to the workspace once per workgroup and a second
+// kernel adds them in a fixed order.
+#include <math.h>
+#include <stdlib.h>
+
+#include "block_norm.h"
+#include "ffn_internal.h"
+
+using namespace gemm_rs::ffn;
+
+namespace {
+
+constexpr int64_t kMaxCols = 16384;
+
+struct NormArgs {
+    int64_t rows, cols, rows_per_gate;
+    int64_t ld_x, ld_y, ld_x_out, ld_u, ld_dx_out, ld_du, ld_dx, ld_dy;
+    float res_scale, weight_offset, eps_post, eps_pre;
+    int32_t has_y, post, pre, gated, param_f32;
+    const void *x, *y, *w_post, *gate, *w_pre;
+    void *x_out, *u;
+    float *u_scale;
+    const void *dx_out, *du;
+    void *dx, *dy;
+    float *dgate;
+    // backward: rows_per_wg consecutive rows per workgroup; its partial sums
+    // at part[wg][0 dw_post, 1 dw_pre, 2 gate head, 3 gate tail][cols]
+    int64_t rows_per_wg;
+    float *part;
+};
+
+template <int VEC>
+__device__ __forceinline__ void load_param(const NormArgs &a, const void *p, int64_t i, float add,
+                                           float *out) {
+    if (a.param_f32) {
+        Raw<true, VEC> r;
+        load_raw(r, p, i);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) out[e] = raw_at(r, e) + add;
+    } else {
+        Raw<false, VEC> r;
+        load_raw(r, p, i);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) out[e] = raw_at(r, e) + add;
+    }
+}
+
+// THREADS threads hold a row of up to THREADS * EPT columns: thread t has
+// the VEC columns from (k * THREADS + t) * VEC for k < EPT / VEC.
+template <int VEC, int EPT, int THREADS, bool SF, bool YF, bool QUANT>
+__global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
+    constexpr int VPT = EPT / VEC;
+    __shared__ float slots[2 * 16];
+    int turn = 0;
+    const int tid = threadIdx.x;
+    const float inv_cols = 1.0f / (float)a.cols;
+
+    float w_post[EPT], w_pre[EPT], gate[EPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
+        float *wo = w_post + k * VEC, *wp = w_pre + k * VEC, *g = gate + k * VEC;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) wo[e] = wp[e] = g[e] = 1.0f;
+        if (c < a.cols) {
+            if (a.post) load_param<VEC>(a, a.w_post, c, a.weight_offset, wo);
+            if (a.pre) load_param<VEC>(a, a.w_pre, c, a.weight_offset, wp);
+        }
+    }
+    int64_t gate_row = -1;
+    for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+        Raw<SF, VEC> xr[VPT];
+        Raw<YF, VEC> yr[VPT];
+        float x[EPT], y[EPT];
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
+            xr[k] = Raw<SF, VEC>{};
+            yr[k] = Raw<YF, VEC>{};
+            if (c < a.cols) {
+                load_raw(xr[k], a.x, row * a.ld_x + c);
+                if (a.has_y) load_raw(yr[k], a.y, row * a.ld_y + c);
+            }
+        }
+        if (a.gated && row / a.rows_per_gate != gate_row) {
+            gate_row = row / a.rows_per_gate;
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
+                if (c < a.cols) load_param<VEC>(a, a.gate, gate_row * a.cols + c, 0.0f, gate + k * VEC);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                x[k * VEC + e] = raw_at(xr[k], e);
+                y[k * VEC + e] = raw_at(yr[k], e);
+            }
+        if (a.has_y) {
+            float r2 = 1.0f;
+            if (a.post) {
+                float s[1] = {0.0f};
+#pragma unroll
+                for (int i = 0; i < EPT; ++i) s[0] += y[i] * y[i];
+                block_join<Sum, THREADS, 1>(s, slots, turn);
+                r2 = 1.0f / sqrtf(s[0] * inv_cols + a.eps_post);
+            }
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) {
+                    const int i = k * VEC + e;
+                    x[i] = a.res_scale * x[i] + gate[i] * (y[i] * r2 * w_post[i]);
+                }
+                if (c < a.cols) store_vec<SF, VEC>(a.x_out, row * a.ld_x_out + c, x + k * VEC);
+            }
+        }
+        if (!a.pre) continue;
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                s[0] += x[k * VEC + e] * x[k * VEC + e];   // columns past the row hold zeros
+        block_join<Sum, THREADS, 1>(s, slots, turn);
+        const float r1 = 1.0f / sqrtf(s[0] * inv_cols + a.eps_pre);
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) x[i] = x[i] * r1 * w_pre[i];
+        if constexpr (QUANT) {
+            float m[1] = {0.0f};
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) m[0] = MaxBits::join(m[0], fabsf(x[i]));
+            block_join<MaxBits, THREADS, 1>(m, slots, turn);
+            const QuantRow q = quant_row(m[0]);
+            if (tid == 0) a.u_scale[row] = q.scale;
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
+                if (c >= a.cols) continue;
+                int8_t *to = (int8_t *)a.u + row * a.ld_u + c;
+                if constexpr (VEC == 8) {
+                    u32x2_t w = {0u, 0u};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        w[e >> 2] |= (uint32_t)(quant_one(q, x[k * VEC + e]) & 0xff) << (8 * (e & 3));
+                    *(u32x2_t *)to = w;
+                } else {
+                    *to = (int8_t)quant_one(q, x[k]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
+                if (c < a.cols) store_vec<YF, VEC>(a.u, row * a.ld_u + c, x + k * VEC);
+            }
+        }
+    }
+}
+
+template <int VEC, int EPT, int THREADS, bool SF, bool YF>
+__global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
+    constexpr int VPT = EPT / VEC;
+    __shared__ float slots[2 * 3 * 16];
+    int turn = 0;
+    const int tid = threadIdx.x;
+    const float inv_cols = 1.0f / (float)a.cols;
+    const int64_t first = (int64_t)blockIdx.x * a.rows_per_wg;
+    int64_t last = first + a.rows_per_wg;
+    if (last > a.rows) last = a.rows;
+
+    float w_post[EPT], w_pre[EPT], gate[EPT];
+    float s_post[EPT], s_pre[EPT], s_gate[EPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
+        float *wo = w_post + k * VEC, *wp = w_pre + k * VEC;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            const int i = k * VEC + e;
+            wo[e] = wp[e] = gate[i] = 1.0f;
+            s_post[i] = s_pre[i] = s_gate[i] = 0.0f;
+        }
+        if (c < a.cols) {
+            if (a.post) load_param<VEC>(a, a.w_post, c, a.weight_offset, wo);
+            if (a.pre) load_param<VEC>(a, a.w_pre, c, a.weight_offset, wp);
+        }
+    }
+    int64_t gate_row = -1;
+    // A gate row's sum: whole if all its rows are this workgroup's, else a
+    // part: the head slot for the group of the first row, the tail slot for
+    // a later one.
+    auto flush_gate = [&](int64_t g) {
+        const int64_t lo = g * a.rows_per_gate;
+        int64_t hi = lo + a.rows_per_gate;
+        if (hi > a.rows) hi = a.rows;
+        const bool whole = lo >= first && hi <= last;
+        float *to = whole ? a.dgate + g * a.cols
+                          : a.part + ((int64_t)blockIdx.x * 4 + (g == first / a.rows_per_gate ? 2 : 3)) * a.cols;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
+            if (c < a.cols) store_vec<true, VEC>(to, c, s_gate + k * VEC);
+        }
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) s_gate[i] = 0.0f;
+    };
+
+    for (int64_t row = first; row < last; ++row) {
+        Raw<SF, VEC> xr[VPT], dr[VPT];
+        Raw<YF, VEC> yr[VPT], ur[VPT];
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
+            xr[k] = dr[k] = Raw<SF, VEC>{};
+            yr[k] = ur[k] = Raw<YF, VEC>{};
+            if (c < a.cols) {
+                if (a.pre) {
+                    load_raw(xr[k], a.x_out, row * a.ld_x_out + c);
+                    load_raw(ur[k], a.du, row * a.ld_du + c);
+                }
+                if (a.has_y) load_raw(yr[k], a.y, row * a.ld_y + c);
+                if (a.dx_out) load_raw(dr[k], a.dx_out, row * a.ld_dx_out + c);
+            }
+        }
+        if (a.gated && row / a.rows_per_gate != gate_row) {
+            if (gate_row >= 0) flush_gate(gate_row);
+            gate_row = row / a.rows_per_gate;
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
+                if (c < a.cols) load_param<VEC>(a, a.gate, gate_row * a.cols + c, 0.0f, gate + k * VEC);
+            }
+        }
+        float s[3] = {0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const int i = k * VEC + e;
+                const float x = raw_at(xr[k], e), y = raw_at(yr[k], e);
+                s[0] += x * x;
+                s[1] += raw_at(ur[k], e) * w_pre[i] * x;
+                s[2] += y * y;
+            }
+        block_join<Sum, THREADS, 3>(s, slots, turn);
+        const float r1 = 1.0f / sqrtf(s[0] * inv_cols + a.eps_pre);
+        const float m1 = s[1] * inv_cols * r1;          // mean(a * xh)
+        const float r2 = a.post ? 1.0f / sqrtf(s[2] * inv_cols + a.eps_post) : 1.0f;
+        float d[EPT];
+        float t[1] = {0.0f};
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
+            float dx[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const int i = k * VEC + e;
+                const float xh = raw_at(xr[k], e) * r1, du = raw_at(ur[k], e);
+                d[i] = raw_at(dr[k], e);
+                if (a.pre) d[i] += r1 * (du * w_pre[i] - xh * m1);
+                s_pre[i] += du * xh;
+                dx[e] = a.has_y ? a.res_scale * d[i] : d[i];
+            }
+            if (c < a.cols) store_vec<SF, VEC>(a.dx, row * a.ld_dx + c, dx);
+        }
+        if (!a.has_y) continue;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                const int i = k * VEC + e;
+                const float yh = raw_at(yr[k], e) * r2;
+                s_gate[i] += d[i] * (yh * w_post[i]);
+                d[i] *= gate[i];                         // dz
+                s_post[i] += d[i] * yh;
+                d[i] *= w_post[i];                       // b
+                t[0] += d[i] * yh;
+            }
+        float m2 = 0.0f;
+        if (a.post) {
+            block_join<Sum, THREADS, 1>(t, slots, turn);
+            m2 = t[0] * inv_cols;                        // mean(b * yh)
+        }
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
+            float dy[VEC];
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                dy[e] = r2 * (d[k * VEC + e] - raw_at(yr[k], e) * r2 * m2);
+            if (c < a.cols) store_vec<YF, VEC>(a.dy, row * a.ld_dy + c, dy);
+        }
+    }
+    if (a.gated && gate_row >= 0) flush_gate(gate_row);
+    float *part = a.part + (int64_t)blockIdx.x * 4 * a.cols;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+        const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
+        if (c >= a.cols) continue;
+        if (a.post) store_vec<true, VEC>(part, c, s_post + k * VEC);
+        if (a.pre) store_vec<true, VEC>(part + a.cols, c, s_pre + k * VEC);
+    }
+}
+
+// Adds the workgroups' partial sums.  blockIdx.y: 0 dw_post, 1 dw_pre, and
+// 2 + w the gate row that lies across the end of workgroup w's rows, if w's
+// is the first such end in that row.  64 columns per workgroup; 16 threads per
+// column take every 16th partial, then add up in a fixed order.
+__global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a, int64_t wgs, float *dw_post,
+                                                         float *dw_pre) {
+    __shared__ float sums[16][64];
+    const int col = threadIdx.x & 63, lane = threadIdx.x >> 6;
+    const int64_t c = (int64_t)blockIdx.x * 64 + col;
+    const int y = blockIdx.y;
+    float *to = nullptr;
+    int64_t lo = 0, hi = wgs, g = -1;
+    if (y == 0) to = dw_post;
+    else if (y == 1) to = dw_pre;
+    else {
+        const int64_t w = y - 2, end = (w + 1) * a.rows_per_wg;   // < rows: w is not the last
+        g = end / a.rows_per_gate;
+        const int64_t start = g * a.rows_per_gate;
+        if (start == end || start < w * a.rows_per_wg) return;
+        int64_t stop = start + a.rows_per_gate;
+        if (stop > a.rows) stop = a.rows;
+        to = a.dgate + g * a.cols;
+        lo = w;
+        hi = (stop + a.rows_per_wg - 1) / a.rows_per_wg;
+    }
+    if (!to) return;
+    float s = 0.0f;
+    if (c < a.cols)
+        for (int64_t w = lo + lane; w < hi; w += 16) {
+            int slot = y;
+            if (g >= 0) slot = (w * a.rows_per_wg) / a.rows_per_gate == g ? 2 : 3;
+            s += a.part[(w * 4 + slot) * a.cols + c];
+        }
+    sums[lane][col] = s;
+    __syncthreads();
+    if (lane == 0 && c < a.cols) {
+#pragma unroll
+        for (int l = 1; l < 16; ++l) s += sums[l][col];
+        to[c] = s;
+    }
+}
+
+__global__ void norm_zero_kernel(float *a, float *b, int64_t n) {
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i < n) {
+        if (a) a[i] = 0.0f;
+        if (b) b[i] = 0.0f;
+    }
+}
+
+// Threads and columns per thread for a row length.
+struct Shape {
+    int threads, ept;
+};
+Shape shape_of(int64_t cols, bool vec) {
+    if (vec && cols <= 512) return {64, 8};
+    if (cols <= 2048) return {256, 8};
+    if (vec && cols <= 4096) return {512, 8};
+    if (cols <= 8192) return {1024, 8};
+    return {1024, 16};
+}
+
+template <int VEC, int EPT, int THREADS>
+void launch_forward(const NormArgs &a, bool sf, bool yf, bool quant, int64_t grid, hipStream_t s) {
+    auto go = [&](auto *kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(THREADS), 0, s, a);
+    };
+    if (quant) {
+        if (sf && yf) go(norm_forward_kernel<VEC, EPT, THREADS, true, true, true>);
+        else if (sf) go(norm_forward_kernel<VEC, EPT, THREADS, true, false, true>);
+        else if (yf) go(norm_forward_kernel<VEC, EPT, THREADS, false, true, true>);
+        else go(norm_forward_kernel<VEC, EPT, THREADS, false, false, true>);
+    } else {
+        if (sf && yf) go(norm_forward_kernel<VEC, EPT, THREADS, true, true, false>);
+        else if (sf) go(norm_forward_kernel<VEC, EPT, THREADS, true, false, false>);
+        else if (yf) go(norm_forward_kernel<VEC, EPT, THREADS, false, true, false>);
+        else go(norm_forward_kernel<VEC, EPT, THREADS, false, false, false>);
+    }
+}
+
+template <int VEC, int EPT, int THREADS>
+void launch_backward(const NormArgs &a, bool sf, bool yf, int64_t grid, hipStream_t s) {
+    auto go = [&](auto *kernel) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(THREADS), 0, s, a);
+    };
+    if (sf && yf) go(norm_backward_kernel<VEC, EPT, THREADS, true, true>);
+    else if (sf) go(norm_backward_kernel<VEC, EPT, THREADS, true, false>);
+    else if (yf) go(norm_backward_kernel<VEC, EPT, THREADS, false, true>);
+    else go(norm_backward_kernel<VEC, EPT, THREADS, false, false>);
+}
+
+// Calls f with the kernel shape's constants.
+template <class F>
+void with_shape(int64_t cols, bool vec, F f) {
+    const Shape sh = shape_of(cols, vec);
+    if (vec) {
+        if (sh.threads == 64) f(std::integral_constant<int, 8>{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 64>{});
+        else if (sh.threads == 256) f(std::integral_constant<int, 8>{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 256>{});
+        else if (sh.threads == 512) f(std::integral_constant<int, 8>{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 512>{});
+        else if (sh.ept == 8) f(std::integral_constant<int, 8>{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 1024>{});
+        else f(std::integral_constant<int, 8>{}, std::integral_constant<int, 16>{}, std::integral_constant<int, 1024>{});
+    } else {
+        if (sh.threads == 256) f(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 256>{});
+        else if (sh.ept == 8) f(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 1024>{});
+        else f(std::integral_constant<int, 1>{}, std::integral_constant<int, 16>{}, std::integral_constant<int, 1024>{});
+    }
+}
+
+// Most workgroups of a backward launch: enough to fill the CUs' wave slots
+// that the kernel's registers allow (16 waves per CU), and no more, because
+// each writes 4 rows of partial sums.
+int64_t backward_wgs(int64_t rows, int64_t cols, bool vec) {
+    const int64_t most = (int64_t)kCus * 1024 / shape_of(cols, vec).threads;
+    const int64_t cap = most < 2048 ? most : 2048;
+    return rows < cap ? rows : cap;
+}
+
+}  // namespace
+
+struct block_norm_plan_s {
+    block_norm_desc_t d;
+    int device;
+    float *part;
+    int64_t part_bytes;
+};
+
+namespace {
+
+bool flag(int32_t v) { return v == 0 || v == 1; }
+
+int validate(const block_norm_desc_t &d) {
+    if (d.rows < 1 || d.cols < 1 || d.rows_per_gate < 0 || d.pad != 0) return GEMM_RS_ERR_INVALID_ARG;
+    if (!known_type(d.dtype) || !known_type(d.stream_dtype) || !known_type(d.param_dtype))
+        return GEMM_RS_ERR_INVALID_ARG;
+    if (!flag(d.has_y) || !flag(d.post) || !flag(d.pre) || !flag(d.quant) || !flag(d.backward))
+        return GEMM_RS_ERR_INVALID_ARG;
+    if (!d.has_y && (d.post || d.rows_per_gate || !d.pre)) return GEMM_RS_ERR_INVALID_ARG;
+    if (d.quant && (!d.pre || d.backward)) return GEMM_RS_ERR_INVALID_ARG;
+    if (!isfinite(d.res_scale) || !isfinite(d.weight_offset) || !isfinite(d.eps_post) ||
+        !isfinite(d.eps_pre) || d.eps_post < 0 || d.eps_pre < 0)
+        return GEMM_RS_ERR_INVALID_ARG;
+    const int64_t lds[] = {d.ld_x, d.ld_y, d.ld_x_out, d.ld_u, d.ld_dx_out, d.ld_du, d.ld_dx, d.ld_dy};
+    for (int64_t ld : lds)
+        if (ld != 0 && ld < d.cols) return GEMM_RS_ERR_INVALID_ARG;
+    for (int64_t ld : lds)
+        if (ld > INT32_MAX) return GEMM_RS_ERR_UNSUPPORTED;
+    if (d.cols > kMaxCols || d.rows > INT32_MAX || d.rows_per_gate > INT32_MAX)
+        return GEMM_RS_ERR_UNSUPPORTED;
+    return GEMM_RS_OK;
+}
+
+NormArgs args_of(const block_norm_desc_t &d, int64_t rows) {
+    NormArgs a = {};
+    a.rows = rows;
+    a.cols = d.cols;
+    a.rows_per_gate = d.rows_per_gate ? d.rows_per_gate : 1;
+    auto ld = [&](int64_t v) { return v ? v : d.cols; };
+    a.ld_x = ld(d.ld_x);
+    a.ld_y = ld(d.ld_y);
+    a.ld_x_out = ld(d.ld_x_out);
+    a.ld_u = ld(d.ld_u);
+    a.ld_dx_out = ld(d.ld_dx_out);
+    a.ld_du = ld(d.ld_du);
+    a.ld_dx = ld(d.ld_dx);
+    a.ld_dy = ld(d.ld_dy);
+    a.res_scale = d.res_scale;
+    a.weight_offset = d.weight_offset;
+    a.eps_post = d.eps_post;
+    a.eps_pre = d.eps_pre;
+    a.has_y = d.has_y;
+    a.post = d.post;
+    a.pre = d.pre;
+    a.gated = d.rows_per_gate > 0;
+    a.param_f32 = d.param_dtype == GEMM_RS_F32;
+    return a;
+}
+
+// A pointer is there exactly if it is wanted, at a multiple of its element.
+bool fits(const void *p, bool wanted, size_t elem) {
+    return wanted ? (p && aligned(p, elem)) : !p;
+}
+
+// Whether rows at p, ld elements apart, can be accessed 8 elements (8
+// bytes of int8) at a time.
+bool wide(const void *p, int64_t ld, size_t elem) {
+    return !p || (ld % 8 == 0 && aligned(p, elem == 1 ? 8 : 16));
+}
+
+}  // namespace
+
+extern "C" {
+
+int block_norm_plan(const block_norm_desc_t *desc, block_norm_plan_t *out) {
+    if (!desc || !out) return GEMM_RS_ERR_INVALID_ARG;
+    *out = nullptr;
+    const int rc = validate(*desc);
+    if (rc != GEMM_RS_OK) return rc;
+    block_norm_plan_s *p = (block_norm_plan_s *)calloc(1, sizeof(block_norm_plan_s));
+    if (!p) return GEMM_RS_ERR_HIP;
+    p->d = *desc;
+    if (hipGetDevice(&p->device) != hipSuccess) {
+        free(p);
+        return GEMM_RS_ERR_HIP;
+    }
+    if (desc->backward) {
+        // the narrow kernels' rows may be cut into more workgroups
+        const int64_t a = backward_wgs(desc->rows, desc->cols, false);
+        const int64_t b = backward_wgs(desc->rows, desc->cols, true);
+        p->part_bytes = (a > b ? a : b) * 4 * desc->cols * (int64_t)sizeof(float);
+        if (hipMalloc((void **)&p->part, p->part_bytes) != hipSuccess) {
+            (void)hipGetLastError();
+            free(p);
+            return GEMM_RS_ERR_HIP;
+        }
+    }
+    *out = p;
+    return GEMM_RS_OK;
+}
+
+int block_norm_run(block_norm_plan_t p, const void *x, const void *y, const void *w_post,
+                   const void *gate, const void *w_pre, void *x_out, void *u, void *u_scale,
+                   int64_t rows, void *stream) {
+    if (!p || !on_device(p->device)) return GEMM_RS_ERR_INVALID_ARG;
+    const block_norm_desc_t &d = p->d;
+    if (rows < 0 || rows > d.rows) return GEMM_RS_ERR_INVALID_ARG;
+    const size_t se = type_bytes(d.stream_dtype), ye = type_bytes(d.dtype), pe = type_bytes(d.param_dtype);
+    const size_t ue = d.quant ? 1 : ye;
+    if (!fits(x, true, se) || !fits(y, d.has_y, ye) || !fits(w_post, d.post, pe) ||
+        !fits(gate, d.rows_per_gate > 0, pe) || !fits(w_pre, d.pre, pe) ||
+        !fits(x_out, d.has_y, se) || !fits(u, d.pre, ue) || !fits(u_scale, d.quant, 4))
+        return GEMM_RS_ERR_INVALID_ARG;
+    if (rows == 0) return GEMM_RS_OK;
+    NormArgs a = args_of(d, rows);
+    if (x == x_out && a.ld_x != a.ld_x_out) return GEMM_RS_ERR_INVALID_ARG;
+    a.x = x;
+    a.y = y;
+    a.w_post = w_post;
+    a.gate = gate;
+    a.w_pre = w_pre;
+    a.x_out = x_out;
+    a.u = u;
+    a.u_scale = (float *)u_scale;
+    const bool vec = d.cols % 8 == 0 && wide(x, a.ld_x, se) && wide(y, a.ld_y, ye) &&
+                     wide(w_post, 8, pe) && wide(gate, 8, pe) && wide(w_pre, 8, pe) &&
+                     wide(x_out, a.ld_x_out, se) && wide(u, a.ld_u, ue);
+    with_shape(d.cols, vec, [&](auto v, auto ept, auto threads) {
+        const int64_t most = (int64_t)kCus * 2048 / threads.value;
+        launch_forward<v.value, ept.value, threads.value>(
+            a, d.stream_dtype == GEMM_RS_F32, d.dtype == GEMM_RS_F32, d.quant != 0,
+            rows < most ? rows : most, (hipStream_t)stream);
+    });
+    return hipGetLastError() == hipSuccess ? GEMM_RS_OK : GEMM_RS_ERR_HIP;
+}
+
+int block_norm_backward(block_norm_plan_t p, const void *dx_out, const void *du, const void *x_out,
+                        const void *y, const void *w_post, const void *gate, const void *w_pre,
+                        void *dx, void *dy, void *dw_post, void *dgate, void *dw_pre, int64_t rows,
+                        void *stream) {
+    if (!p || !on_device(p->device) || !p->d.backward) return GEMM_RS_ERR_INVALID_ARG;
+    const block_norm_desc_t &d = p->d;
+    if (rows < 0 || rows > d.rows) return GEMM_RS_ERR_INVALID_ARG;
+    const size_t se = type_bytes(d.stream_dtype), ye = type_bytes(d.dtype), pe = type_bytes(d.param_dtype);
+    const bool gated = d.rows_per_gate > 0;
+    if (!fits(dx_out, dx_out || !d.pre, se) || !fits(du, d.pre, ye) || !fits(x_out, d.pre, se) ||
+        !fits(y, d.has_y, ye) || !fits(w_post, d.post, pe) || !fits(gate, gated, pe) ||
+        !fits(w_pre, d.pre, pe) || !fits(dx, true, se) || !fits(dy, d.has_y, ye) ||
+        !fits(dw_post, d.post, 4) || !fits(dgate, gated, 4) || !fits(dw_pre, d.pre, 4))
+        return GEMM_RS_ERR_INVALID_ARG;
+    hipStream_t s = (hipStream_t)stream;
+    if (rows == 0) {
+        if (dw_post || dw_pre)
+            hipLaunchKernelGGL(norm_zero_kernel, dim3((unsigned)((d.cols + 255) / 256)), dim3(256), 0, s,
+                               (float *)dw_post, (float *)dw_pre, d.cols);
+        return hipGetLastError() == hipSuccess ? GEMM_RS_OK : GEMM_RS_ERR_HIP;
+    }
+    NormArgs a = args_of(d, rows);
+    a.x_out = (void *)x_out;
+    a.dx_out = dx_out;
+    a.du = du;
+    a.y = y;
+    a.w_post = w_post;
+    a.gate = gate;
+    a.w_pre = w_pre;
+    a.dx = dx;
+    a.dy = dy;
+    a.dgate = (float *)dgate;
+    a.part = p->part;
+    const bool vec = d.cols % 8 == 0 && wide(x_out, a.ld_x_out, se) && wide(y, a.ld_y, ye) &&
+                     wide(dx_out, a.ld_dx_out, se) && wide(du, a.ld_du, ye) &&
+                     wide(w_post, 8, pe) && wide(gate, 8, pe) && wide(w_pre, 8, pe) &&
+                     wide(dx, a.ld_dx, se) && wide(dy, a.ld_dy, ye) && wide(dgate, 8, 4);
+    int64_t wgs = backward_wgs(rows, d.cols, vec);
+    a.rows_per_wg = (rows + wgs - 1) / wgs;
+    wgs = (rows + a.rows_per_wg - 1) / a.rows_per_wg;
+    with_shape(d.cols, vec, [&](auto v, auto ept, auto threads) {
+        launch_backward<v.value, ept.value, threads.value>(
+            a, d.stream_dtype == GEMM_RS_F32, d.dtype == GEMM_RS_F32, wgs, s);
+    });
+    if (hipGetLastError() != hipSuccess) return GEMM_RS_ERR_HIP;
+    // gate rows lie across workgroups' ends unless the runs are whole groups
+    const bool split = gated && wgs > 1 && a.rows_per_wg % a.rows_per_gate != 0;
+    if (d.post || d.pre || split) {
+        const unsigned ny = 2 + (split ? (unsigned)(wgs - 1) : 0);
+        hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)((d.cols + 63) / 64), ny), dim3(1024), 0, s,
+                           a, wgs, (float *)dw_post, (float *)dw_pre);
+    }
+    return hipGetLastError() == hipSuccess ? GEMM_RS_OK : GEMM_RS_ERR_HIP;
+}
+
+int block_norm_query(block_norm_plan_t p, block_norm_info_t *info) {
+    if (!p || !info) return GEMM_RS_ERR_INVALID_ARG;
+    const block_norm_desc_t &d = p->d;
+    info->gate_rows = d.rows_per_gate ? (d.rows + d.rows_per_gate - 1) / d.rows_per_gate : 0;
+    info->workspace_bytes = p->part_bytes;
+    return GEMM_RS_OK;
+}
+
+int block_norm_destroy(block_norm_plan_t p) {
+    if (!p) return GEMM_RS_OK;
+    int cur = -1;
+    bool switched = false;
+    if (p->part && hipGetDevice(&cur) == hipSuccess && cur != p->device)
+        switched = hipSetDevice(p->device) == hipSuccess;
+    // teardown is best effort: a failure here leaves nothing to undo
+    if (p->part) (void)hipFree(p->part);
+    if (switched) (void)hipSetDevice(cur);
+    free(p);
+    return GEMM_RS_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,188 @@
+// Shared by the FFN sub-layer's operators (block norm, 8-bit product,
+// products grouped by expert): element access, row reductions, host checks.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gemm_rs.h"
+
+namespace gemm_rs {
+namespace ffn {
+
+constexpr int kCus = 256;   // MI355X: 8 XCDs x 32 CUs
+
+// work is only enqueued while the plan's device is current
+inline bool on_device(int device) {
+    int cur = -1;
+    return hipGetDevice(&cur) == hipSuccess && cur == device;
+}
+
+inline bool aligned(const void *p, size_t bytes) { return ((uintptr_t)p % bytes) == 0; }
+
+inline bool known_type(int32_t t) { return t == GEMM_RS_BF16 || t == GEMM_RS_F32; }
+inline size_t type_bytes(int32_t t) { return t == GEMM_RS_F32 ? 4 : 2; }
+
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// round to nearest even (NaN stays NaN)
+__device__ __forceinline__ uint32_t to_bf16(float x) {
+    return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    return to_bf16(a) | (to_bf16(b) << 16);
+}
+
+// VEC elements as they lie in memory: 8 elements from a 16-byte aligned
+// address, or one.  Kept raw until used, so that a row read ahead costs the
+// registers of its storage type only.
+template <bool F32, int VEC> struct Raw;
+template <> struct Raw<true, 8> { u32x4_t a, b; };
+template <> struct Raw<false, 8> { u32x4_t a; };
+template <> struct Raw<true, 1> { float a; };
+template <> struct Raw<false, 1> { uint16_t a; };
+
+template <bool F32, int VEC>
+__device__ __forceinline__ void load_raw(Raw<F32, VEC> &r, const void *p, int64_t i) {
+    if constexpr (VEC == 8 && F32) {
+        const u32x4_t *q = (const u32x4_t *)((const float *)p + i);
+        r.a = q[0];
+        r.b = q[1];
+    } else if constexpr (VEC == 8) {
+        r.a = *(const u32x4_t *)((const uint16_t *)p + i);
+    } else if constexpr (F32) {
+        r.a = ((const float *)p)[i];
+    } else {
+        r.a = ((const uint16_t *)p)[i];
+    }
+}
+
+template <bool F32, int VEC>
+__device__ __forceinline__ float raw_at(const Raw<F32, VEC> &r, int e) {
+    if constexpr (VEC == 8 && F32)
+        return __uint_as_float(e < 4 ? r.a[e] : r.b[e - 4]);
+    else if constexpr (VEC == 8)
+        return (e & 1) ? bf16_hi(r.a[e >> 1]) : bf16_lo(r.a[e >> 1]);
+    else if constexpr (F32)
+        return r.a;
+    else
+        return bf16_lo(r.a);
+}
+
+template <bool F32, int VEC>
+__device__ __forceinline__ void store_vec(void *p, int64_t i, const float *v) {
+    if constexpr (VEC == 8 && F32) {
+        f32x4_t *q = (f32x4_t *)((float *)p + i);
+        q[0] = f32x4_t{v[0], v[1], v[2], v[3]};
+        q[1] = f32x4_t{v[4], v[5], v[6], v[7]};
+    } else if constexpr (VEC == 8) {
+        u32x4_t w;
+        w[0] = pack_bf16(v[0], v[1]);
+        w[1] = pack_bf16(v[2], v[3]);
+        w[2] = pack_bf16(v[4], v[5]);
+        w[3] = pack_bf16(v[6], v[7]);
+        *(u32x4_t *)((uint16_t *)p + i) = w;
+    } else if constexpr (F32) {
+        ((float *)p)[i] = v[0];
+    } else {
+        ((uint16_t *)p)[i] = (uint16_t)to_bf16(v[0]);
+    }
+}
+
+// A workgroup barrier for LDS hand-offs: waits for this wave's LDS
+// operations but not for its global loads and stores.
+__device__ __forceinline__ void lds_only_barrier() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+
+struct Sum {
+    static __device__ __forceinline__ float join(float a, float b) { return a + b; }
+    static __device__ __forceinline__ float none() { return 0.0f; }
+};
+// Largest bit pattern of a magnitude: as unsigned integers NaN > inf >
+// every finite value, so neither is lost (a float maximum drops NaN).
+struct MaxBits {
+    static __device__ __forceinline__ float join(float a, float b) {
+        const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+        return __uint_as_float(x > y ? x : y);
+    }
+    static __device__ __forceinline__ float none() { return 0.0f; }
+};
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+    return __int_as_float(
+        __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, false));
+}
+
+// One wave's join of a value, in every lane: four steps inside rows of 16
+// lanes (quad permutes and mirrors), then the four rows.
+template <class OP>
+__device__ __forceinline__ float wave_join(float v) {
+    v = OP::join(v, dpp<0xb1>(v));    // lanes 1,0,3,2
+    v = OP::join(v, dpp<0x4e>(v));    // lanes 2,3,0,1
+    v = OP::join(v, dpp<0x141>(v));   // mirror of each 8
+    v = OP::join(v, dpp<0x140>(v));   // mirror of each 16
+    const int i = __float_as_int(v);
+    const float a = __int_as_float(__builtin_amdgcn_readlane(i, 0));
+    const float b = __int_as_float(__builtin_amdgcn_readlane(i, 16));
+    const float c = __int_as_float(__builtin_amdgcn_readlane(i, 32));
+    const float d = __int_as_float(__builtin_amdgcn_readlane(i, 48));
+    return OP::join(OP::join(a, b), OP::join(c, d));
+}
+
+// Join of NV values over a workgroup, in every thread; the order is fixed.
+// `slots` is the workgroup's [2][NV * 16] floats; `turn` alternates between
+// its halves, so one barrier per call is enough: a wave can write the half
+// that call n used only in call n+2, after the barrier of call n+1, which
+// every wave reaches after its reads of call n.
+template <class OP, int THREADS, int NV>
+__device__ __forceinline__ void block_join(float (&v)[NV], float *slots, int &turn) {
+    constexpr int NW = THREADS / 64;
+#pragma unroll
+    for (int n = 0; n < NV; ++n) v[n] = wave_join<OP>(v[n]);
+    if constexpr (NW > 1) {
+        float *s = slots + (turn & 1) * (NV * 16);
+        turn ^= 1;
+        if ((threadIdx.x & 63) == 0)
+#pragma unroll
+            for (int n = 0; n < NV; ++n) s[n * 16 + (threadIdx.x >> 6)] = v[n];
+        lds_only_barrier();
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            float t = s[n * 16];
+#pragma unroll
+            for (int w = 1; w < NW; ++w) t = OP::join(t, s[n * 16 + w]);
+            v[n] = t;
+        }
+    }
+}
+
+// A row's scale and the factor that quantises it, from the bits of its
+// largest magnitude: q = rint(x * pre * inv), scale = max / 127.  `pre` is 1,
+// or 2^64 for rows so small that 127 / max would overflow.
+struct QuantRow {
+    float scale, pre, inv;
+    bool finite;
+};
+__device__ __forceinline__ QuantRow quant_row(float amax) {
+    QuantRow r;
+    r.finite = __float_as_uint(amax) < 0x7f800000u;
+    r.pre = amax < 0x1p-100f ? 0x1p64f : 1.0f;
+    r.scale = r.finite ? amax / 127.0f : __uint_as_float(0x7fc00000u);
+    r.inv = (r.finite && amax > 0.0f) ? 127.0f / (amax * r.pre) : 0.0f;
+    return r;
+}
+__device__ __forceinline__ int quant_one(const QuantRow &r, float x) {
+    if (!r.finite) return 0;
+    // |x * inv| <= 127 up to rounding, which rint takes back to 127
+    return (int)rintf(x * r.pre * r.inv);
+}
+
+}  // namespace ffn
+}  // namespace gemm_rs
