@@ -13,8 +13,8 @@
  *
  * gemm_q8_quantize makes a and a_scale from bfloat16 or float rows:
  *     a_scale[m] = max_k |x[m][k]| / 127
- *     a[m][k]    = round_to_nearest_even(x[m][k] * (127 / max_k |x[m][k]|))
- * A row of zeros gets scale 0 and zeros; a row with a NaN or an infinity
+ *     a[m][k]    = round_to_nearest_even(x[m][k] * (127 * (1 / max_k |x[m][k]|)))
+ * each step in 32-bit floats, rounded to nearest.  A row of zeros gets scale 0 and zeros; a row with a NaN or an infinity
  * gets scale NaN and zeros, so its products are NaN.
  *
  * Status codes and gemm_rs_strerror are those of gemm_rs.h.  All functions

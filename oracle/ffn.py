@@ -82,7 +82,7 @@ def quantize_rows(x32):
         amax = np.abs(row).max()
         if amax > 0:
             scale[i] = amax / np.float32(127)
-            q[i] = np.rint(row * (np.float32(127) / amax)).astype(np.int8)
+            q[i] = np.rint(row * (np.float32(127) * (np.float32(1) / amax))).astype(np.int8)
     return q, scale
 
 

@@ -164,8 +164,8 @@ __device__ __forceinline__ void block_join(float (&v)[NV], float *slots, int &tu
 }
 
 // A row's scale and the factor that quantises it, from the bits of its
-// largest magnitude: q = rint(x * pre * inv), scale = max / 127.  `pre` is 1,
-// or 2^64 for rows so small that 127 / max would overflow.
+// largest magnitude: q = rint(x * pre * inv), inv = 127 * (1 / max), scale =
+// max / 127.  `pre` is 1, or 2^64 for rows so small that inv would overflow.
 struct QuantRow {
     float scale, pre, inv;
     bool finite;
@@ -175,7 +175,7 @@ __device__ __forceinline__ QuantRow quant_row(float amax) {
     r.finite = __float_as_uint(amax) < 0x7f800000u;
     r.pre = amax < 0x1p-100f ? 0x1p64f : 1.0f;
     r.scale = r.finite ? amax / 127.0f : __uint_as_float(0x7fc00000u);
-    r.inv = (r.finite && amax > 0.0f) ? 127.0f / (amax * r.pre) : 0.0f;
+    r.inv = (r.finite && amax > 0.0f) ? 127.0f * (1.0f / (amax * r.pre)) : 0.0f;
     return r;
 }
 __device__ __forceinline__ int quant_one(const QuantRow &r, float x) {

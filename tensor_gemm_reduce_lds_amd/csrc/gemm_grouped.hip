@@ -27,12 +27,13 @@ struct GroupedArgs {
 };
 
 // Rows [lo, hi) of expert e, clipped to 0 <= lo <= hi <= rows.
-__device__ __forceinline__ void group_rows(const GroupedArgs &p, int e, int64_t *lo, int64_t *hi) {
-    const int64_t a = p.offsets[e], b = p.offsets[e + 1];
-    int64_t l = a < 0 ? 0 : a;
-    if (l > p.rows) l = p.rows;
-    int64_t h = b > p.rows ? p.rows : b;
-    if (h < l) h = l;
+__device__ __forceinline__ void group_rows(const GroupedArgs &p, int e, int32_t *lo, int32_t *hi) {
+    const int32_t rows = (int32_t)p.rows;
+    int32_t l = p.offsets[e], h = p.offsets[e + 1];
+    l = l < 0 ? 0 : l;
+    l = l > rows ? rows : l;
+    h = h > rows ? rows : h;
+    h = h < l ? l : h;
     *lo = l;
     *hi = h;
 }
@@ -53,45 +54,69 @@ __device__ __forceinline__ void check_offsets(const GroupedArgs &p) {
 
 struct RowTile {
     int e;
-    int64_t lo, hi;     // the expert's rows
-    int64_t row0;       // the tile's first row
+    int32_t lo, hi;     // the expert's rows
+    int32_t row0;       // the tile's first row
     int tn;             // column tile
 };
 
-// The tile of logical workgroup b for row tiles of BM rows, by each wave for
+// Workgroup b of n, in an order that gives each XCD one run of the n tiles
+// (the hardware deals workgroups out to the 8 XCDs in turn): neighbouring
+// tiles share an operand, so they should share an L2.  A bijection of [0, n).
+__device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t n) {
+    const uint32_t x = b % 8, j = b / 8, q = n / 8, r = n % 8;
+    return x * q + (x < r ? x : r) + j;
+}
+
+// The tile of workgroup b for row tiles of bm rows, found by each wave for
 // itself (64 experts at a time, a prefix sum over the lanes); false if there
-// are fewer tiles.  Expert after expert, an expert's column tiles one after
-// another, its row tiles inside a column.
+// are fewer tiles.  Tiles run expert by expert; inside an expert, row tiles
+// in groups of 8, a group column by column, so that the tiles that run
+// together read few rows of A and columns of B.
 __device__ __forceinline__ bool find_row_tile(const GroupedArgs &p, int bm, uint32_t b, RowTile *t) {
     const int lane = threadIdx.x & 63;
-    uint32_t before = 0;      // tiles of the experts of earlier turns
-    for (int e0 = 0; e0 < p.E; e0 += 64) {
-        const int e = e0 + lane;
-        int64_t lo = 0, hi = 0;
-        if (e < p.E) group_rows(p, e, &lo, &hi);
-        const uint32_t rt = (uint32_t)((hi - lo + bm - 1) / bm);
-        uint32_t upto = rt * (uint32_t)p.tiles_n;
+    const uint32_t tn = (uint32_t)p.tiles_n;
+    auto turn = [&](int e0, uint32_t *rt, uint32_t *upto) {
+        int32_t lo = 0, hi = 0;
+        if (e0 + lane < p.E) group_rows(p, e0 + lane, &lo, &hi);
+        *rt = ((uint32_t)(hi - lo) + (uint32_t)bm - 1u) / (uint32_t)bm;
+        uint32_t v = *rt * tn;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
-            const uint32_t v = __shfl_up(upto, d);
-            if (lane >= d) upto += v;
+            const uint32_t u = __shfl_up(v, d);
+            if (lane >= d) v += u;
         }
-        upto += before;
-        const uint64_t past = __ballot(upto > b);
+        *upto = v;
+    };
+    uint32_t rt, upto, total = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 64) {
+        turn(e0, &rt, &upto);
+        total += __shfl(upto, 63);
+    }
+    if (b >= total) return false;
+    b = xcd_run(b, total);
+    uint32_t before = 0;      // tiles of the experts of earlier turns
+    for (int e0 = 0; e0 < p.E; e0 += 64) {
+        if (p.E > 64) turn(e0, &rt, &upto);
+        const uint32_t end = upto + before;
+        const uint64_t past = __ballot(end > b);
         if (past) {
             const int src = __builtin_ctzll(past);
             const uint32_t n = __shfl(rt, src);
-            const uint32_t j = b - (__shfl(upto, src) - n * (uint32_t)p.tiles_n);
+            const uint32_t j = b - (__shfl(end, src) - n * tn);
             // overlapping (clipped) groups can wrap the 32-bit prefix: such
             // a tile is left out, every other lies inside its expert
-            if (j >= n * (uint32_t)p.tiles_n) return false;
-            t->e = e0 + src;
+            if (j >= n * tn) return false;
+            t->e = __builtin_amdgcn_readfirstlane(e0 + src);
             group_rows(p, t->e, &t->lo, &t->hi);
-            t->tn = (int)(j / n);
-            t->row0 = t->lo + (int64_t)(j % n) * bm;
+            t->lo = __builtin_amdgcn_readfirstlane(t->lo);
+            t->hi = __builtin_amdgcn_readfirstlane(t->hi);
+            const uint32_t g = j / (8 * tn), in = j - g * 8 * tn;
+            const uint32_t rows = n - g * 8 < 8 ? n - g * 8 : 8;
+            t->tn = __builtin_amdgcn_readfirstlane(in / rows);
+            t->row0 = t->lo + __builtin_amdgcn_readfirstlane((g * 8 + in % rows) * (uint32_t)bm);
             return true;
         }
-        before = __shfl(upto, 63);
+        before += __shfl(upto, 63);
     }
     return false;
 }
@@ -105,7 +130,8 @@ __global__ __launch_bounds__(256) void grouped_narrow_kernel(GroupedArgs p) {
     __shared__ __attribute__((aligned(16))) uint16_t As[64 * PITCH], Bs[64 * PITCH];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     if (blockIdx.x == 0 && wave == 0) check_offsets(p);
-    int64_t lo, hi, m0, n0, m_end, k_len;
+    int32_t lo, hi;
+    int64_t m0, n0, m_end, k_len;
     int e;
     if constexpr (OP == GEMM_GROUPED_TN) {
         const int tiles = p.tiles_m * p.tiles_n;
@@ -171,6 +197,113 @@ __global__ __launch_bounds__(256) void grouped_narrow_kernel(GroupedArgs p) {
                 *c = (uint16_t)to_bf16(x);
             }
         }
+    }
+}
+
+// 8 columns of a row of C.
+__device__ __forceinline__ void store8(const GroupedArgs &p, int64_t row, int64_t n, const int (&v)[8]) {
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = __int_as_float(v[e]);
+    const int64_t at = row * p.ldc + n;
+    if (p.out_f32) {
+        if (p.accumulate) {
+            Raw<true, 8> c;
+            load_raw(c, p.C, at);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] += raw_at(c, e);
+        }
+        store_vec<true, 8>(p.C, at, x);
+    } else {
+        if (p.accumulate) {
+            Raw<false, 8> c;
+            load_raw(c, p.C, at);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] += raw_at(c, e);
+        }
+        store_vec<false, 8>(p.C, at, x);
+    }
+}
+
+// Sizes, strides and addresses that are multiples of 8 elements.
+template <int OP, int BM, int BN, int WGM, int WGN, int STAGES>
+using GroupedTile = Tile<f32x16_t, BM, BN, WGM, WGN, OP == GEMM_GROUPED_TN, OP != GEMM_GROUPED_NT, STAGES>;
+
+template <int OP, int BM, int BN, int WGM, int WGN, int STAGES>
+__global__ __launch_bounds__(64 * WGM * WGN) void grouped_tile_kernel(GroupedArgs p) {
+    using T = GroupedTile<OP, BM, BN, WGM, WGN, STAGES>;
+    extern __shared__ __attribute__((aligned(1024))) char smem_generic[];
+    lds_t *smem = (lds_t *)smem_generic;
+    if (blockIdx.x == 0 && threadIdx.x < 64) check_offsets(p);
+    T tile;
+    if constexpr (OP == GEMM_GROUPED_TN) {
+        // XCD x takes the x-th eighth of every expert's tiles, so the XCDs'
+        // shares are equal however uneven the groups are
+        const int tiles = p.tiles_m * p.tiles_n, per = (tiles + 7) / 8;
+        const int j = blockIdx.x / 8, e = j / per;
+        const int t = (int)(blockIdx.x % 8) * per + (j - e * per);
+        if (t >= tiles) return;
+        const int64_t m0 = (int64_t)(t / p.tiles_n) * BM, n0 = (int64_t)(t % p.tiles_n) * BN;
+        int32_t lo, hi;
+        group_rows(p, e, &lo, &hi);
+        lo = __builtin_amdgcn_readfirstlane(lo);
+        hi = __builtin_amdgcn_readfirstlane(hi);
+        if (hi == lo && p.accumulate) return;
+        const int32_t m_left = (int32_t)(p.K - m0 < BM ? p.K - m0 : BM);
+        const int32_t n_left = (int32_t)(p.N - n0 < BN ? p.N - n0 : BN);
+        const Operand a = {(const char *)(p.A + (int64_t)lo * p.lda + m0), p.lda * 2, m_left * 2};
+        const Operand b = {(const char *)(p.B + (int64_t)lo * p.ldb + n0), p.ldb * 2, n_left * 2};
+        tile.template run<2>(smem, a, b, hi - lo);
+        tile.store(smem, [&](int r, int c, const int (&v)[8]) {
+            if (r < m_left && c < n_left) store8(p, (int64_t)e * p.K + m0 + r, n0 + c, v);
+        });
+    } else {
+        RowTile t;
+        if (!find_row_tile(p, BM, blockIdx.x, &t)) return;
+        const int64_t n0 = (int64_t)t.tn * BN;
+        const int32_t m_left = t.hi - t.row0 < BM ? t.hi - t.row0 : BM;
+        const int32_t n_left = (int32_t)(p.N - n0 < BN ? p.N - n0 : BN);
+        const Operand a = {(const char *)(p.A + (int64_t)t.row0 * p.lda), p.lda * 2, m_left};
+        const Operand b = OP == GEMM_GROUPED_NN
+            ? Operand{(const char *)(p.B + (int64_t)t.e * p.K * p.ldb + n0), p.ldb * 2, n_left * 2}
+            : Operand{(const char *)(p.B + ((int64_t)t.e * p.N + n0) * p.ldb), p.ldb * 2, n_left};
+        tile.template run<2>(smem, a, b, (int32_t)p.K);
+        tile.store(smem, [&](int r, int c, const int (&v)[8]) {
+            if (r < m_left && c < n_left) store8(p, (int64_t)t.row0 + r, n0 + c, v);
+        });
+    }
+}
+
+template <int OP, int BM, int BN, int WGM, int WGN, int STAGES>
+hipError_t launch_tile(GroupedArgs &a, hipStream_t s) {
+    using T = GroupedTile<OP, BM, BN, WGM, WGN, STAGES>;
+    a.tiles_n = (int32_t)((a.N + BN - 1) / BN);
+    a.tiles_m = (int32_t)((a.K + BM - 1) / BM);
+    int64_t blocks;
+    if (OP == GEMM_GROUPED_TN) blocks = (((int64_t)a.tiles_m * a.tiles_n + 7) / 8) * 8 * a.E;
+    else blocks = (a.rows / BM + (a.E < a.rows ? a.E : a.rows)) * a.tiles_n;
+    return launch_lds<grouped_tile_kernel<OP, BM, BN, WGM, WGN, STAGES>>(blocks, T::THREADS, T::LDS_BYTES, s, a);
+}
+
+template <int OP>
+hipError_t launch_op(GroupedArgs &a, bool wide, hipStream_t s) {
+    if (!wide) {
+        a.tiles_n = (int32_t)((a.N + 63) / 64);
+        a.tiles_m = (int32_t)((a.K + 63) / 64);
+        const int64_t row_tiles = OP == GEMM_GROUPED_TN ? (int64_t)a.E * a.tiles_m
+                                                        : a.rows / 64 + (a.E < a.rows ? a.E : a.rows);
+        hipLaunchKernelGGL(grouped_narrow_kernel<OP>, dim3((unsigned)(row_tiles * a.tiles_n)), dim3(256), 0, s, a);
+        return hipGetLastError();
+    }
+    if constexpr (OP == GEMM_GROUPED_TN) {
+        const int64_t big = (int64_t)a.E * ((a.K + 255) / 256) * ((a.N + 255) / 256);
+        if (big >= kCus) return launch_tile<OP, 256, 256, 2, 4, 2>(a, s);
+        return launch_tile<OP, 128, 128, 2, 2, 2>(a, s);
+    } else {
+        const int64_t avg = a.rows / a.E;      // the sizes themselves are on the device
+        if (avg >= 192) return launch_tile<OP, 256, 256, 2, 4, 2>(a, s);
+        if (avg >= 48) return launch_tile<OP, 128, 128, 2, 2, 2>(a, s);
+        return launch_tile<OP, 32, 128, 1, 4, 6>(a, s);
     }
 }
 
@@ -255,16 +388,13 @@ int gemm_grouped_run(gemm_grouped_plan_t p, const void *A, const void *B, const 
     a.C = C;
     a.err = p->err;
     hipStream_t s = (hipStream_t)stream;
-    a.tiles_n = (int32_t)((d.N + 63) / 64);
-    a.tiles_m = (int32_t)((d.K + 63) / 64);
-    const int64_t row_tiles = d.op == GEMM_GROUPED_TN ? (int64_t)d.E * a.tiles_m
-                                                      : rows / 64 + (d.E < rows ? d.E : rows);
-    const dim3 grid((unsigned)(row_tiles * a.tiles_n));
-    auto go = [&](auto *kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a); };
-    if (d.op == GEMM_GROUPED_NN) go(grouped_narrow_kernel<GEMM_GROUPED_NN>);
-    else if (d.op == GEMM_GROUPED_NT) go(grouped_narrow_kernel<GEMM_GROUPED_NT>);
-    else go(grouped_narrow_kernel<GEMM_GROUPED_TN>);
-    return hipGetLastError() == hipSuccess ? GEMM_RS_OK : GEMM_RS_ERR_HIP;
+    const int64_t c_elems = d.out_dtype == GEMM_RS_F32 ? 4 : 8;
+    const bool wide = d.N % 8 == 0 && d.K % 8 == 0 && d.lda % 8 == 0 && d.ldb % 8 == 0 &&
+                      d.ldc % c_elems == 0 && aligned(A, 16) && aligned(B, 16) && aligned(C, 16);
+    const hipError_t e = d.op == GEMM_GROUPED_NN   ? launch_op<GEMM_GROUPED_NN>(a, wide, s)
+                         : d.op == GEMM_GROUPED_NT ? launch_op<GEMM_GROUPED_NT>(a, wide, s)
+                                                   : launch_op<GEMM_GROUPED_TN>(a, wide, s);
+    return e == hipSuccess ? GEMM_RS_OK : GEMM_RS_ERR_HIP;
 }
 
 int gemm_grouped_status(gemm_grouped_plan_t p, void *stream, int32_t *detail) {
