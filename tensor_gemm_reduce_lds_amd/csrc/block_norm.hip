@@ -343,6 +343,7 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a, int64_t wgs
     if (!to) return;
     float s = 0.0f;
     if (c < a.cols)
+#pragma unroll 8
         for (int64_t w = lo + lane; w < hi; w += 16) {
             int slot = y;
             if (g >= 0) slot = (w * a.rows_per_wg) / a.rows_per_gate == g ? 2 : 3;

@@ -59,14 +59,6 @@ struct RowTile {
     int tn;             // column tile
 };
 
-// Workgroup b of n, in an order that gives each XCD one run of the n tiles
-// (the hardware deals workgroups out to the 8 XCDs in turn): neighbouring
-// tiles share an operand, so they should share an L2.  A bijection of [0, n).
-__device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t n) {
-    const uint32_t x = b % 8, j = b / 8, q = n / 8, r = n % 8;
-    return x * q + (x < r ? x : r) + j;
-}
-
 // The tile of workgroup b for row tiles of bm rows, found by each wave for
 // itself (64 experts at a time, a prefix sum over the lanes); false if there
 // are fewer tiles.  Tiles run expert by expert; inside an expert, row tiles

@@ -20,6 +20,7 @@
 
 #include <mutex>
 #include <type_traits>
+#include <utility>
 
 #include "ffn_internal.h"
 
@@ -46,6 +47,12 @@ __device__ __forceinline__ f32x16_t mma(i32x4_t a, i32x4_t b, f32x16_t acc) {
 }
 __device__ __forceinline__ i32x16_t mma(i32x4_t a, i32x4_t b, i32x16_t acc) {
     return __builtin_amdgcn_mfma_i32_32x32x32_i8(b, a, acc, 0, 0, 0);
+}
+// One 16 x 16 block, 64 deep in int8: 16 bytes per lane of each operand (row
+// lane % 16, the lane/16-th 16 bytes).  Swapped as above: a lane holds output
+// row lane % 16, columns 4*(lane/16) + 0..3.
+__device__ __forceinline__ i32x4_t mma16(i32x4_t a, i32x4_t b, i32x4_t acc) {
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(b, a, acc, 0, 0, 0);
 }
 
 // Raw buffer descriptor: 48-bit base, `bytes` records.  A load at or past
@@ -86,6 +93,14 @@ __device__ __forceinline__ void wait_groups(int groups) {
     }
 }
 
+// Workgroup b of n, in an order that gives each XCD one run of the n tiles
+// (the hardware deals workgroups out to the 8 XCDs in turn): neighbouring
+// tiles share an operand, so they should share an L2.  A bijection of [0, n).
+__device__ __forceinline__ uint32_t xcd_run(uint32_t b, uint32_t n) {
+    const uint32_t x = b % 8, j = b / 8, q = n / 8, r = n % 8;
+    return x * q + (x < r ? x : r) + j;
+}
+
 // One operand of a tile.  Row operand (COL false): `span` output rows from
 // base, ld bytes apart, contraction along the row.  Column operand (COL
 // true): contraction rows ld bytes apart, of which `span` bytes belong to
@@ -114,6 +129,7 @@ struct Tile {
     static constexpr int AI = A_BYTES / 1024 / DW, BI = B_BYTES / 1024 / DW;
     static_assert(AI * DW * 1024 == A_BYTES && BI * DW * 1024 == B_BYTES, "whole loads per wave");
     static_assert(WM % 32 == 0 && WN % 32 == 0, "whole blocks per wave");
+    static_assert(DW * 8 == 32, "the row swizzle alternates with the load");
     static_assert(!A_COL || BM >= 128, "column swizzle needs 16 chunks per row");
     static_assert(!B_COL || BN >= 128, "column swizzle needs 16 chunks per row");
     static_assert(LDS_BYTES <= 160 * 1024, "LDS");
@@ -126,29 +142,46 @@ struct Tile {
 
     ACC acc[FM][FN];
 
-    // Byte offset (inside a step's window) that this lane loads in issue i.
-    template <bool COL, int B>
-    static __device__ __forceinline__ uint32_t load_offset(const Operand &o, int i, int dwave, int lane) {
-        if constexpr (COL) {
-            constexpr int CPR = B / 8;                  // chunks per contraction row
-            const int k = (i * DW + dwave) * (64 / CPR) + lane / CPR;
-            return (uint32_t)(k * o.ld + ((lane % CPR) ^ col_swz(k)) * 16);
-        } else {
-            int m = (i * DW + dwave) * 8 + lane / 8;
-            const int c = (lane & 7) ^ row_swz(m);
-            if (m >= o.span) m = o.span - 1;            // rows past the end repeat the last
-            return (uint32_t)(m * o.ld + c * 16);
-        }
+    // Load i of an operand covers the rows from i * ROWS of its window: the
+    // descriptor moves by ROWS rows and keeps the window's end, so rows past it
+    // read as zero, and a lane's offset takes at most two values (the row
+    // swizzle alternates with i).
+    template <bool COL, int B> static constexpr int load_rows() {
+        return COL ? DW * 64 / (B / 8) : DW * 8;
     }
-    // Descriptor of step kt, of which `left` (at most KE) elements, or rows of
-    // a column operand, are valid.
+    template <bool COL, int B>
+    static __device__ __forceinline__ int load_chunk(int odd, int dwave, int lane) {
+        if constexpr (COL) return (lane % (B / 8)) ^ col_swz(dwave * (64 / (B / 8)) + lane / (B / 8));
+        else return (lane & 7) ^ row_swz(odd * 32 + dwave * 8 + lane / 8);
+    }
+    template <bool COL, int B>
+    static __device__ __forceinline__ uint32_t load_offset(const Operand &o, int odd, int dwave, int lane) {
+        const int row = COL ? dwave * (64 / (B / 8)) + lane / (B / 8) : dwave * 8 + lane / 8;
+        return (uint32_t)row * (uint32_t)o.ld + (uint32_t)load_chunk<COL, B>(odd, dwave, lane) * 16u;
+    }
+    // Bytes of step kt's window, of which `left` (at most KE) elements, or
+    // rows of a column operand, are valid; and its base.
     template <bool COL, int ELEM>
-    static __device__ __forceinline__ i32x4_t window(const Operand &o, int kt, int left) {
-        if constexpr (COL)
-            return buffer_of(o.base + (int64_t)kt * 64 * o.ld, (uint32_t)(left - 1) * (uint32_t)o.ld + (uint32_t)o.span);
-        else
-            return buffer_of(o.base + (int64_t)kt * 128,
-                             (uint32_t)(o.span - 1) * (uint32_t)o.ld + (uint32_t)(left * ELEM));
+    static __device__ __forceinline__ uint32_t window_bytes(const Operand &o, int left) {
+        if constexpr (COL) return (uint32_t)(left - 1) * (uint32_t)o.ld + (uint32_t)o.span;
+        else return (uint32_t)(o.span - 1) * (uint32_t)o.ld + (uint32_t)(left * ELEM);
+    }
+    template <bool COL>
+    static __device__ __forceinline__ const char *window_base(const Operand &o, int kt) {
+        return o.base + (COL ? (int64_t)kt * 64 * o.ld : (int64_t)kt * 128);
+    }
+    template <int I, bool COL, int B>
+    static __device__ __forceinline__ void load_part(const Operand &o, const char *base, uint32_t bytes,
+                                                     uint32_t voff, uint32_t lds, int dwave) {
+        const uint32_t skip = (uint32_t)I * load_rows<COL, B>() * (uint32_t)o.ld;
+        load_to_lds(buffer_of(base + skip, bytes > skip ? bytes - skip : 0u), voff,
+                    lds + (I * DW + dwave) * 1024);
+    }
+    template <bool COL, int B, int... I>
+    static __device__ __forceinline__ void load_all(std::integer_sequence<int, I...>, const Operand &o,
+                                                    const char *base, uint32_t bytes,
+                                                    const uint32_t (&voff)[2], uint32_t lds, int dwave) {
+        (load_part<I, COL, B>(o, base, bytes, voff[COL ? 0 : I & 1], lds, dwave), ...);
     }
 
     // acc = A . B over a contraction of `k` elements (of a column operand:
@@ -164,101 +197,92 @@ struct Tile {
         const int KT = (int)(((uint32_t)k + KE - 1) / KE);
         const int dwave = wave < DW ? wave : 0;
 
-        uint32_t a_voff[AI], b_voff[BI];
-#pragma unroll
-        for (int i = 0; i < AI; ++i) a_voff[i] = load_offset<A_COL, BM>(a, i, dwave, lane);
-#pragma unroll
-        for (int i = 0; i < BI; ++i) b_voff[i] = load_offset<B_COL, BN>(b, i, dwave, lane);
+        const uint32_t a_voff[2] = {load_offset<A_COL, BM>(a, 0, dwave, lane),
+                                    A_COL ? 0u : load_offset<A_COL, BM>(a, 1, dwave, lane)};
+        const uint32_t b_voff[2] = {load_offset<B_COL, BN>(b, 0, dwave, lane),
+                                    B_COL ? 0u : load_offset<B_COL, BN>(b, 1, dwave, lane)};
 
         auto issue = [&](int kt, int st) __attribute__((always_inline)) {
             if (wave >= DW) return;                     // wave-uniform
             const int left = k - kt * KE < KE ? k - kt * KE : KE;
-            const uint32_t As = smem_base + st * A_BYTES;
-            const uint32_t Bs = smem_base + STAGES * A_BYTES + st * B_BYTES;
-            const i32x4_t ra = window<A_COL, ELEM>(a, kt, left), rb = window<B_COL, ELEM>(b, kt, left);
-            if (left == KE) {
-#pragma unroll
-                for (int i = 0; i < AI; ++i) load_to_lds(ra, a_voff[i], As + (i * DW + dwave) * 1024);
-#pragma unroll
-                for (int i = 0; i < BI; ++i) load_to_lds(rb, b_voff[i], Bs + (i * DW + dwave) * 1024);
-            } else {
+            uint32_t av[2] = {a_voff[0], a_voff[1]}, bv[2] = {b_voff[0], b_voff[1]};
+            if (left < KE) {
                 // the last step of a contraction that is no multiple of KE:
                 // row chunks past its end are sent past the descriptor (a
                 // column operand's rows past it lie there already)
                 const int chunks = left * ELEM / 16;
-                auto cut = [&](uint32_t voff, int i) __attribute__((always_inline)) {
-                    const int m = (i * DW + dwave) * 8 + lane / 8;
-                    return ((lane & 7) ^ row_swz(m)) < chunks ? voff : 0xfffffff0u;
-                };
 #pragma unroll
-                for (int i = 0; i < AI; ++i)
-                    load_to_lds(ra, A_COL ? a_voff[i] : cut(a_voff[i], i), As + (i * DW + dwave) * 1024);
-#pragma unroll
-                for (int i = 0; i < BI; ++i)
-                    load_to_lds(rb, B_COL ? b_voff[i] : cut(b_voff[i], i), Bs + (i * DW + dwave) * 1024);
+                for (int odd = 0; odd < 2; ++odd) {
+                    if (!A_COL && load_chunk<A_COL, BM>(odd, dwave, lane) >= chunks) av[odd] = 0xfffffff0u;
+                    if (!B_COL && load_chunk<B_COL, BN>(odd, dwave, lane) >= chunks) bv[odd] = 0xfffffff0u;
+                }
             }
+            load_all<A_COL, BM>(std::make_integer_sequence<int, AI>{}, a, window_base<A_COL>(a, kt),
+                                window_bytes<A_COL, ELEM>(a, left), av, smem_base + st * A_BYTES, dwave);
+            load_all<B_COL, BN>(std::make_integer_sequence<int, BI>{}, b, window_base<B_COL>(b, kt),
+                                window_bytes<B_COL, ELEM>(b, left), bv,
+                                smem_base + STAGES * A_BYTES + st * B_BYTES, dwave);
         };
 
-        // LDS offsets of this lane's fragments inside a stage's tile.  Row
-        // operand: 16 bytes of row lane % 32.  Column operand: two
-        // transposing reads of 4 x 16 blocks, of which this lane addresses
-        // row e, columns 4q..4q+3.
-        int a_off[FM][KS][A_COL ? 2 : 1], b_off[FN][KS][B_COL ? 2 : 1];
+        // LDS addresses of this lane's fragments: few registers, and constants
+        // for the reads' immediate field.  Row operand: 16 bytes of row
+        // lane % 32; block i lies i * 4096 further, with the row swizzle of
+        // i's parity.  Column operand: two transposing reads of 4 x 16 blocks,
+        // of which this lane addresses row te, columns 4 tq..4 tq + 3; slices and
+        // halves lie whole rows further, blocks differ in the swizzled chunk.
+        constexpr int B_AT = STAGES * A_BYTES;
         const int grp = lane >> 4, te = (lane & 15) >> 2, tq = lane & 3;
-        auto col_off = [&](int x, int ks, int h, int width) __attribute__((always_inline)) {
-            const int kk = ks * 16 + 8 * (grp >> 1) + 4 * h + te;
-            const int n = x + 16 * (grp & 1) + 4 * tq;
-            return kk * (width * 2) + (((n >> 3) ^ col_swz(kk)) << 4) + ((n & 7) << 1);
+        lds_t *a_at[A_COL ? 1 : KS][A_COL ? FM : 2], *b_at[B_COL ? 1 : KS][B_COL ? FN : 2];
+        auto col_at = [&](lds_t *tile, int x, int width) __attribute__((always_inline)) {
+            const int n = x + 16 * (grp & 1) + 4 * tq, kk = 8 * (grp >> 1) + te;
+            return tile + (kk * (width * 2) + (((n >> 3) ^ col_swz(kk)) << 4) + ((n & 7) << 1));
         };
-        auto row_off = [&](int x, int ks) __attribute__((always_inline)) {
+        auto row_at = [&](lds_t *tile, int x, int odd, int ks) __attribute__((always_inline)) {
             const int m = x + (lane & 31), c = 2 * ks + (lane >> 5);
-            return m * 128 + ((c ^ row_swz(m)) << 4);
+            return tile + (m * 128 + ((c ^ row_swz(m) ^ (4 * odd)) << 4));
         };
+        if constexpr (A_COL) {
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
+            for (int i = 0; i < FM; ++i) a_at[0][i] = col_at(smem, wm * WM + i * 32, BM);
+        } else {
 #pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                if constexpr (A_COL) {
-                    a_off[i][ks][0] = col_off(wm * WM + i * 32, ks, 0, BM);
-                    a_off[i][ks][1] = col_off(wm * WM + i * 32, ks, 1, BM);
-                } else {
-                    a_off[i][ks][0] = row_off(wm * WM + i * 32, ks);
-                }
-            }
+            for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                if constexpr (B_COL) {
-                    b_off[j][ks][0] = STAGES * A_BYTES + col_off(wn * WN + j * 32, ks, 0, BN);
-                    b_off[j][ks][1] = STAGES * A_BYTES + col_off(wn * WN + j * 32, ks, 1, BN);
-                } else {
-                    b_off[j][ks][0] = STAGES * A_BYTES + row_off(wn * WN + j * 32, ks);
-                }
-            }
+                for (int odd = 0; odd < 2; ++odd) a_at[ks][odd] = row_at(smem, wm * WM, odd, ks);
+        }
+        if constexpr (B_COL) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j) b_at[0][j] = col_at(smem + B_AT, wn * WN + j * 32, BN);
+        } else {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int odd = 0; odd < 2; ++odd) b_at[ks][odd] = row_at(smem + B_AT, wn * WN, odd, ks);
         }
 #pragma unroll
         for (int i = 0; i < FM; ++i)
 #pragma unroll
             for (int j = 0; j < FN; ++j) acc[i][j] = ACC{};
 
-        auto col_read = [&](lds_t *at, const int (&off)[2]) __attribute__((always_inline)) {
+        auto col_read = [&](lds_t *at, int width) __attribute__((always_inline)) {
             typedef __attribute__((address_space(3))) i16x4_t lds_i16x4;
-            const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(at + off[0]));
-            const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(at + off[1]));
+            const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)at);
+            const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(at + 4 * width * 2));
             const i16x8_t both = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
             return __builtin_bit_cast(i32x4_t, both);
         };
+        typedef __attribute__((address_space(3))) i32x4_t lds_i32x4;
         auto load_frags = [&](int st, int ks, i32x4_t (&af)[FM], i32x4_t (&bf)[FN])
             __attribute__((always_inline)) {
-            lds_t *const SA = smem + st * A_BYTES, *const SB = smem + st * B_BYTES;
 #pragma unroll
             for (int i = 0; i < FM; ++i) {
-                if constexpr (A_COL) af[i] = col_read(SA, a_off[i][ks]);
-                else af[i] = *(__attribute__((address_space(3))) i32x4_t *)(SA + a_off[i][ks][0]);
+                if constexpr (A_COL) af[i] = col_read(a_at[0][i] + st * A_BYTES + ks * 16 * BM * 2, BM);
+                else af[i] = *(lds_i32x4 *)(a_at[ks][i & 1] + st * A_BYTES + i * 4096);
             }
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
-                if constexpr (B_COL) bf[j] = col_read(SB, b_off[j][ks]);
-                else bf[j] = *(__attribute__((address_space(3))) i32x4_t *)(SB + b_off[j][ks][0]);
+                if constexpr (B_COL) bf[j] = col_read(b_at[0][j] + st * B_BYTES + ks * 16 * BN * 2, BN);
+                else bf[j] = *(lds_i32x4 *)(b_at[ks][j & 1] + st * B_BYTES + j * 4096);
             }
         };
         // Fragments are double-buffered in registers: the next slice's LDS
