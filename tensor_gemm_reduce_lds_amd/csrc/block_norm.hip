@@ -315,12 +315,13 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
     }
 }
 
-// Adds the workgroups' partial sums.  blockIdx.y: 0 dw_post, 1 dw_pre, and
-// 2 + w the gate row that lies across the end of workgroup w's rows, if w's
-// is the first such end in that row.  64 columns per workgroup; 16 threads per
-// column take every 16th partial, then add up in a fixed order.
-__global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a, int64_t wgs, float *dw_post,
-                                                         float *dw_pre) {
+// Adds the workgroups' partial sums.  blockIdx.y: 0 dw_post, 1 dw_pre, then the
+// gate rows whose rows are not all one workgroup's: by gate row (by_group), or
+// by the workgroup w whose end is the first to lie inside the gate row, where
+// that makes fewer workgroups.  64 columns per workgroup; 16 threads per column
+// take every 16th partial, then add up in a fixed order.
+__global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a, int64_t wgs, int by_group,
+                                                         float *dw_post, float *dw_pre) {
     __shared__ float sums[16][64];
     const int col = threadIdx.x & 63, lane = threadIdx.x >> 6;
     const int64_t c = (int64_t)blockIdx.x * 64 + col;
@@ -330,15 +331,14 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a, int64_t wgs
     if (y == 0) to = dw_post;
     else if (y == 1) to = dw_pre;
     else {
-        const int64_t w = y - 2, end = (w + 1) * a.rows_per_wg;   // < rows: w is not the last
-        g = end / a.rows_per_gate;
+        g = by_group ? y - 2 : (int64_t)(y - 1) * a.rows_per_wg / a.rows_per_gate;
         const int64_t start = g * a.rows_per_gate;
-        if (start == end || start < w * a.rows_per_wg) return;
         int64_t stop = start + a.rows_per_gate;
         if (stop > a.rows) stop = a.rows;
-        to = a.dgate + g * a.cols;
-        lo = w;
+        lo = start / a.rows_per_wg;
         hi = (stop + a.rows_per_wg - 1) / a.rows_per_wg;
+        if (hi - lo < 2 || (!by_group && lo != y - 2)) return;   // whole, or another's
+        to = a.dgate + g * a.cols;
     }
     if (!to) return;
     float s = 0.0f;
@@ -618,9 +618,11 @@ int block_norm_backward(block_norm_plan_t p, const void *dx_out, const void *du,
     // gate rows lie across workgroups' ends unless the runs are whole groups
     const bool split = gated && wgs > 1 && a.rows_per_wg % a.rows_per_gate != 0;
     if (d.post || d.pre || split) {
-        const unsigned ny = 2 + (split ? (unsigned)(wgs - 1) : 0);
+        const int64_t gates = (rows + a.rows_per_gate - 1) / a.rows_per_gate;
+        const bool by_group = gates < wgs - 1;
+        const unsigned ny = 2 + (split ? (unsigned)(by_group ? gates : wgs - 1) : 0);
         hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)((d.cols + 63) / 64), ny), dim3(1024), 0, s,
-                           a, wgs, (float *)dw_post, (float *)dw_pre);
+                           a, wgs, (int)by_group, (float *)dw_post, (float *)dw_pre);
     }
     return hipGetLastError() == hipSuccess ? GEMM_RS_OK : GEMM_RS_ERR_HIP;
 }

@@ -290,11 +290,11 @@ hipError_t launch_op(GroupedArgs &a, bool wide, hipStream_t s) {
     if constexpr (OP == GEMM_GROUPED_TN) {
         const int64_t big = (int64_t)a.E * ((a.K + 255) / 256) * ((a.N + 255) / 256);
         if (big >= kCus) return launch_tile<OP, 256, 256, 2, 4, 2>(a, s);
-        return launch_tile<OP, 128, 128, 2, 2, 2>(a, s);
+        return launch_tile<OP, 128, 128, 2, 2, 4>(a, s);
     } else {
         const int64_t avg = a.rows / a.E;      // the sizes themselves are on the device
         if (avg >= 192) return launch_tile<OP, 256, 256, 2, 4, 2>(a, s);
-        if (avg >= 48) return launch_tile<OP, 128, 128, 2, 2, 2>(a, s);
+        if (avg >= 48) return launch_tile<OP, 128, 128, 2, 2, 4>(a, s);
         return launch_tile<OP, 32, 128, 1, 4, 6>(a, s);
     }
 }

@@ -218,7 +218,7 @@ hipError_t launch_product(const Q8Args &q, hipStream_t s) {
     }
     const int64_t big = ((q.M + 255) / 256) * ((q.N + 255) / 256);
     if (big >= kCus * 3 / 4) return launch_tile<256, 256, 2, 4, 2>(q, s);
-    return launch_tile<128, 128, 2, 2, 2>(q, s);
+    return launch_tile<128, 128, 2, 2, 4>(q, s);
 }
 
 int validate(const gemm_q8_desc_t &d) {
