@@ -246,7 +246,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_tile_kernel(GroupedArg
         const Operand a = {(const char *)(p.A + (int64_t)lo * p.lda + m0), p.lda * 2, m_left * 2};
         const Operand b = {(const char *)(p.B + (int64_t)lo * p.ldb + n0), p.ldb * 2, n_left * 2};
         tile.template run<2>(smem, a, b, hi - lo);
-        tile.store(smem, [&](int r, int c, const int (&v)[8]) {
+        tile.template store<8>(smem, [&](int r, int c, const int (&v)[8]) {
             if (r < m_left && c < n_left) store8(p, (int64_t)e * p.K + m0 + r, n0 + c, v);
         });
     } else {
@@ -260,7 +260,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_tile_kernel(GroupedArg
             ? Operand{(const char *)(p.B + (int64_t)t.e * p.K * p.ldb + n0), p.ldb * 2, n_left * 2}
             : Operand{(const char *)(p.B + ((int64_t)t.e * p.N + n0) * p.ldb), p.ldb * 2, n_left};
         tile.template run<2>(smem, a, b, (int32_t)p.K);
-        tile.store(smem, [&](int r, int c, const int (&v)[8]) {
+        tile.template store<8>(smem, [&](int r, int c, const int (&v)[8]) {
             if (r < m_left && c < n_left) store8(p, (int64_t)t.row0 + r, n0 + c, v);
         });
     }

@@ -48,91 +48,141 @@ __global__ __launch_bounds__(64 * WGM * WGN) void q8_tile_kernel(Q8Args p) {
     const Operand a = {(const char *)p.a + m0 * p.lda, p.lda, m_left};
     const Operand w = {(const char *)p.w + n0 * p.ldw, p.ldw, n_left};
     tile.template run<1>(smem, a, w, (int32_t)p.K);
-    // a lane's 8 columns are the same in every row it stores
-    const int c0 = (int)(threadIdx.x % (BN / 8)) * 8;
-    float sw[8], bias[8];
+    if (p.wide_out && n_left % 8 == 0) {
+        // a lane's 8 columns are the same in every row it stores
+        const int c0 = (int)(threadIdx.x % (BN / 8)) * 8;
+        float sw[8], bias[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int64_t n = n0 + (c0 + e < n_left ? c0 + e : n_left - 1);
-        sw[e] = p.w_scale[n];
-        bias[e] = p.bias ? p.bias[n] : 0.0f;
-    }
-    tile.store(smem, [&](int r, int c, const int (&v)[8]) {
-        if (r >= m_left || c >= n_left) return;
-        const int64_t m = m0 + r;
-        const float sa = p.a_scale[m];
-        float x[8];
+        for (int e = 0; e < 8; ++e) {
+            const int64_t n = n0 + (c0 < n_left ? c0 : 0) + e;
+            sw[e] = p.w_scale[n];
+            bias[e] = p.bias ? p.bias[n] : 0.0f;
+        }
+        tile.template store<8>(smem, [&](int r, int c, const int (&v)[8]) {
+            if (r >= m_left || c >= n_left) return;
+            const int64_t m = m0 + r;
+            const float sa = p.a_scale[m];
+            float x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = scaled(v[e], sa, sw[e], p.bias ? &bias[e] : nullptr);
-        if (p.wide_out && c + 8 <= n_left) {
+            for (int e = 0; e < 8; ++e) x[e] = scaled(v[e], sa, sw[e], p.bias ? &bias[e] : nullptr);
             if (p.out_f32) store_vec<true, 8>(p.D, m * p.ldd + n0 + c, x);
             else store_vec<false, 8>(p.D, m * p.ldd + n0 + c, x);
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (c + e < n_left) store_one(p, m, n0 + c + e, x[e]);
-        }
-    });
+        });
+    } else {
+        tile.template store<1>(smem, [&](int r, int c, const int (&v)[1]) {
+            if (r >= m_left || c >= n_left) return;
+            const int64_t m = m0 + r, n = n0 + c;
+            store_one(p, m, n, scaled(v[0], p.a_scale[m], p.w_scale[n], p.bias ? p.bias + n : nullptr));
+        });
+    }
 }
 
-// Few rows: 16 channels and up to MB * 16 rows per workgroup, the contraction
-// split over its 8 waves.  Every byte of w is used by one wave only, so
-// operands go straight to registers, 64 bytes of each row per matrix
-// operation; the waves' sums (integers: exact in any order) meet in LDS.
-template <int MB>
-__global__ __launch_bounds__(512) void q8_rows_kernel(Q8Args p) {
-    constexpr int NW = 8, U = MB <= 2 ? 8 : 4;      // steps whose loads are in flight together
-    __shared__ __attribute__((aligned(16))) int32_t part[NW][MB * 16][16];
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t n0 = (int64_t)blockIdx.x * 16;
-    const int r = lane & 15, chunk = (lane >> 4) * 16;
-    const int64_t n = n0 + r < p.N ? n0 + r : p.N - 1;
-    const int8_t *wp = p.w + n * p.ldw + chunk;
-    const int8_t *ap[MB];
+// Few rows: NB * 16 channels and up to MB * 16 rows per workgroup.  The
+// contraction is dealt out to the NW waves 128 bytes at a time, and each wave
+// streams its share through S stages of LDS of its own, so no wave waits for
+// another until their sums (integers: exact in any order) meet at the end.
+template <int MB, int NB, int NW, int S>
+struct RowsKernel {
+    static constexpr int LOADS = (MB + NB) * 2;          // of 1 KB (8 rows) per stage
+    static constexpr int STAGE = LOADS * 1024;
+    static constexpr int LDS_BYTES = NW * S * STAGE;
+    static_assert(LDS_BYTES <= 160 * 1024, "LDS");
+    static_assert(MB * NB * 256 * 4 <= S * STAGE, "a wave's sums fit its stages");
+    static_assert((S - 1) * LOADS < 64, "the load counter");
+
+    static __device__ __forceinline__ int swz(int m) { return (m ^ (m >> 3)) & 7; }
+
+    static __device__ void run(const Q8Args &p, lds_t *smem) {
+        const int tid = threadIdx.x, lane = tid & 63;
+        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int n0 = blockIdx.x * NB * 16;
+        const int n_left = (int)p.N - n0 < NB * 16 ? (int)p.N - n0 : NB * 16;
+        const int K = (int)p.K, pieces = (K + 127) / 128;
+        const int mine = pieces > wave ? (pieces - wave + NW - 1) / NW : 0;
+        lds_t *const own = smem + wave * (S * STAGE);
+        const uint32_t own_base = (uint32_t)(size_t)own;
+        const uint32_t a_rows = (uint32_t)(p.M - 1) * (uint32_t)p.lda;      // bytes to the last row
+        const uint32_t w_rows = (uint32_t)(n_left - 1) * (uint32_t)p.ldw;
+        const char *const A = (const char *)p.a, *const W = (const char *)p.w + (int64_t)n0 * p.ldw;
+        // rows past the last lie past the descriptors and read as zero
+        uint32_t voff[LOADS];
 #pragma unroll
-    for (int b = 0; b < MB; ++b) {
-        const int64_t m = b * 16 + r < p.M ? b * 16 + r : p.M - 1;
-        ap[b] = p.a + m * p.lda + chunk;
-    }
-    const int K = (int)p.K, steps = (K + 63) / 64, per = (steps + NW - 1) / NW;
-    const int s0 = wave * per;
-    const int s1 = s0 + per < steps ? s0 + per : steps;
-    i32x4_t acc[MB];
+        for (int i = 0; i < LOADS; ++i) {
+            const int r = (i < 2 * MB ? i : i - 2 * MB) * 8 + lane / 8;
+            voff[i] = (uint32_t)r * (uint32_t)(i < 2 * MB ? p.lda : p.ldw) + (((lane & 7) ^ swz(r)) << 4);
+        }
+        auto issue = [&](int piece, int st) __attribute__((always_inline)) {
+            const int k = (piece * NW + wave) * 128;
+            const int left = K - k < 128 ? K - k : 128;
+            const i32x4_t ra = buffer_of(A + k, a_rows + left), rw = buffer_of(W + k, w_rows + left);
 #pragma unroll
-    for (int b = 0; b < MB; ++b) acc[b] = i32x4_t{0, 0, 0, 0};
-    for (int s = s0; s < s1; s += U) {
-        i32x4_t wf[U], af[U][MB];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int k = (s + u) * 64;
-            // the last step's chunks past K, and steps past this wave's, are 0
-            const bool in = s + u < s1 && k + chunk < K;
-            wf[u] = i32x4_t{0, 0, 0, 0};
-#pragma unroll
-            for (int b = 0; b < MB; ++b) af[u][b] = i32x4_t{0, 0, 0, 0};
-            if (in) {
-                wf[u] = *(const i32x4_t *)(wp + k);
-#pragma unroll
-                for (int b = 0; b < MB; ++b) af[u][b] = *(const i32x4_t *)(ap[b] + k);
+            for (int i = 0; i < LOADS; ++i) {
+                uint32_t v = voff[i];
+                if (left < 128) {                       // chunks past K read as zero too
+                    const int r = (i < 2 * MB ? i : i - 2 * MB) * 8 + lane / 8;
+                    if ((((lane & 7) ^ swz(r)) << 4) >= left) v = 0xfffffff0u;
+                }
+                load_to_lds(i < 2 * MB ? ra : rw, v, own_base + st * STAGE + i * 1024);
             }
+        };
+        typedef __attribute__((address_space(3))) i32x4_t lds_i32x4;
+        typedef __attribute__((address_space(3))) int32_t lds_i32;
+        i32x4_t acc[MB][NB];
+#pragma unroll
+        for (int b = 0; b < MB; ++b)
+#pragma unroll
+            for (int c = 0; c < NB; ++c) acc[b][c] = i32x4_t{0, 0, 0, 0};
+        const int fr = lane & 15;       // fragments: row lane % 16, chunk 4 s + lane / 16
+#pragma unroll
+        for (int s = 0; s < S - 1; ++s)
+            if (s < mine) issue(s, s);
+        int st = 0;
+        for (int i = 0; i < mine; ++i) {
+            wait_groups<LOADS, S - 2>(mine - 1 - i);
+            if (i + S - 1 < mine) issue(i + S - 1, st == 0 ? S - 1 : st - 1);
+            i32x4_t af[2][MB], wf[2][NB];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+#pragma unroll
+                for (int b = 0; b < MB; ++b)
+                    af[s][b] = *(lds_i32x4 *)(own + st * STAGE + (b * 16 + fr) * 128 +
+                                              (((4 * s + (lane >> 4)) ^ swz(b * 16 + fr)) << 4));
+#pragma unroll
+                for (int c = 0; c < NB; ++c)
+                    wf[s][c] = *(lds_i32x4 *)(own + st * STAGE + (MB * 16 + c * 16 + fr) * 128 +
+                                              (((4 * s + (lane >> 4)) ^ swz(c * 16 + fr)) << 4));
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int b = 0; b < MB; ++b)
+#pragma unroll
+                    for (int c = 0; c < NB; ++c) acc[b][c] = mma16(af[s][b], wf[s][c], acc[b][c]);
+            // the reads are done before the next issue overwrites their stage
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            if (++st == S) st = 0;
         }
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int b = 0; b < MB; ++b)
 #pragma unroll
-            for (int b = 0; b < MB; ++b) acc[b] = mma16(af[u][b], wf[u], acc[b]);
+            for (int c = 0; c < NB; ++c)
+                *(lds_i32x4 *)(own + ((b * 16 + fr) * (NB * 16) + c * 16 + (lane >> 4) * 4) * 4) = acc[b][c];
+        __syncthreads();
+        for (int i = tid; i < MB * NB * 256; i += NW * 64) {
+            const int64_t m = i / (NB * 16), n = n0 + i % (NB * 16);
+            int32_t v = 0;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) v += *(lds_i32 *)(smem + w * (S * STAGE) + i * 4);
+            if (m < p.M && n < p.N)
+                store_one(p, m, n, scaled(v, p.a_scale[m], p.w_scale[n], p.bias ? p.bias + n : nullptr));
+        }
     }
-#pragma unroll
-    for (int b = 0; b < MB; ++b) *(i32x4_t *)&part[wave][b * 16 + r][(lane >> 4) * 4] = acc[b];
-    __syncthreads();
-    for (int i = tid; i < MB * 256; i += 512) {
-        const int64_t m = i >> 4, col = n0 + (i & 15);
-        int32_t v = 0;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) v += part[w][i >> 4][i & 15];
-        if (m < p.M && col < p.N)
-            store_one(p, m, col, scaled(v, p.a_scale[m], p.w_scale[col], p.bias ? p.bias + col : nullptr));
-    }
+};
+
+template <int MB, int NB, int NW, int S>
+__global__ __launch_bounds__(NW * 64) void q8_rows_kernel(Q8Args p) {
+    extern __shared__ __attribute__((aligned(1024))) char smem_generic[];
+    RowsKernel<MB, NB, NW, S>::run(p, (lds_t *)smem_generic);
 }
 
 // Rows of up to EPT * THREADS columns, one per workgroup, in registers; EPT
@@ -205,20 +255,46 @@ hipError_t launch_tile(const Q8Args &q, hipStream_t s) {
         ((q.M + BM - 1) / BM) * ((q.N + BN - 1) / BN), T::THREADS, T::LDS_BYTES, s, q);
 }
 
+template <int MB, int NB, int NW, int S>
+hipError_t launch_rows(const Q8Args &q, hipStream_t s) {
+    using R = RowsKernel<MB, NB, NW, S>;
+    return launch_lds<q8_rows_kernel<MB, NB, NW, S>>((q.N + NB * 16 - 1) / (NB * 16), NW * 64, R::LDS_BYTES, s, q);
+}
+
+// Up to 128 rows the product is bound by streaming w: as many workgroups as
+// there are CUs, so 32 channels each where that still makes 256 of them (the
+// rows of a are then read half as often), else 16.  Measured, us for 16 / 32
+// channels: 64 x 8192 x 3584 11.7 / 9.7, 64 x 3584 x 8192 10.5 / 14.1.
+template <int MB, int NW1, int S1, int NW2, int S2>
+hipError_t launch_few(const Q8Args &q, hipStream_t s) {
+    if (q.N >= 32 * kCus) return launch_rows<MB, 2, NW2, S2>(q, s);
+    return launch_rows<MB, 1, NW1, S1>(q, s);
+}
+
 hipError_t launch_product(const Q8Args &q, hipStream_t s) {
-    if (q.M <= 128) {
-        auto go = [&](auto *kernel) {
-            hipLaunchKernelGGL(kernel, dim3((unsigned)((q.N + 15) / 16)), dim3(512), 0, s, q);
-            return hipGetLastError();
-        };
-        if (q.M <= 16) return go(q8_rows_kernel<1>);
-        if (q.M <= 32) return go(q8_rows_kernel<2>);
-        if (q.M <= 64) return go(q8_rows_kernel<4>);
-        return go(q8_rows_kernel<8>);
-    }
-    const int64_t big = ((q.M + 255) / 256) * ((q.N + 255) / 256);
-    if (big >= kCus * 3 / 4) return launch_tile<256, 256, 2, 4, 2>(q, s);
-    return launch_tile<128, 128, 2, 2, 4>(q, s);
+    if (q.M <= 16) return launch_few<1, 8, 4, 8, 3>(q, s);
+    if (q.M <= 32) return launch_few<2, 8, 3, 8, 2>(q, s);
+    if (q.M <= 64) return launch_few<4, 8, 2, 4, 3>(q, s);
+    if (q.M <= 128) return launch_few<8, 4, 2, 4, 2>(q, s);
+    // The tile with the least time: rounds of 256 workgroups times a round's
+    // time, in us measured at K = 3584 (a round costs about as much where it
+    // is not full).  Large tiles read fewer bytes per operation, small ones
+    // fill the CUs when there are few.  Measured, us for 256 x 256, 128 x 128,
+    // 64 x 128, 64 x 64: 8192 x 8192 x 3584 236, 302, 361, 393; 1024 x 3584 x
+    // 8192 79, 47, 53, 62; 512 x 3584 x 8192 79, 39, 31, 36; 256 x 3584 x 8192
+    // 79, 38, 29, 25.
+    auto rounds = [&](int64_t bm, int64_t bn) {
+        return (double)((((q.M + bm - 1) / bm) * ((q.N + bn - 1) / bn) + kCus - 1) / kCus);
+    };
+    const double t256 = 59 * rounds(256, 256), t128 = 19 * rounds(128, 128);
+    const double t64w = 13 * rounds(64, 128), t64 = 2 + 8 * rounds(64, 64);
+    if (t256 <= t128 && t256 <= t64w && t256 <= t64) return launch_tile<256, 256, 2, 4, 2>(q, s);
+    // one round: deep loads, one workgroup per CU; more: two per CU (1000 x
+    // 4096 x 1792, 256 tiles: 15.0 / 16.2 us; 1000 x 4099, 264 tiles: 33.8 / 21.7)
+    if (t128 <= t64w && t128 <= t64)
+        return rounds(128, 128) <= 1 ? launch_tile<128, 128, 2, 4, 4>(q, s) : launch_tile<128, 128, 2, 4, 2>(q, s);
+    if (t64w <= t64) return launch_tile<64, 128, 2, 4, 3>(q, s);
+    return launch_tile<64, 64, 2, 2, 4>(q, s);
 }
 
 int validate(const gemm_q8_desc_t &d) {

@@ -184,6 +184,11 @@ struct Tile {
         (load_part<I, COL, B>(o, base, bytes, voff[COL ? 0 : I & 1], lds, dwave), ...);
     }
 
+    // Steps of a contraction of k elements, ELEM bytes each.
+    template <int ELEM> static __device__ __forceinline__ int steps_of(int32_t k) {
+        return (int)(((uint32_t)k + 128 / ELEM - 1) / (128 / ELEM));
+    }
+
     // acc = A . B over a contraction of `k` elements (of a column operand:
     // rows; ELEM bytes each in a row operand).
     template <int ELEM>
@@ -194,7 +199,7 @@ struct Tile {
         const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int wm = wave / WGN, wn = wave % WGN;
         const uint32_t smem_base = (uint32_t)(size_t)smem;
-        const int KT = (int)(((uint32_t)k + KE - 1) / KE);
+        const int KT = steps_of<ELEM>(k);
         const int dwave = wave < DW ? wave : 0;
 
         const uint32_t a_voff[2] = {load_offset<A_COL, BM>(a, 0, dwave, lane),
@@ -354,23 +359,23 @@ struct Tile {
         if (KT > 0) mmas(1);
     }
 
-    // Hands the tile out as f(row, column, v[8]) for runs of 8 columns, each
-    // run once, whole rows by neighbouring lanes.  Accumulators pass through
-    // LDS one 32-row block row of every wave at a time: the direct layout
-    // would store 8 bytes per row and instruction.  16-byte chunk c of a
-    // staged row r sits at c ^ (r % 16).
-    template <class F>
+    // Hands the tile out as f(row, column, v[RUN]) for runs of RUN columns (8,
+    // or 1 where the output's rows are not aligned), each run once, whole rows
+    // by neighbouring lanes.  Accumulators pass through LDS one 32-row block
+    // row of every wave at a time: the direct layout would store 8 bytes per
+    // row and instruction.  16-byte chunk c of a staged row r sits at
+    // c ^ (r % 16).
+    template <int RUN, class F>
     __device__ __forceinline__ void store(lds_t *smem, F f) const {
+        static_assert(RUN == 8 || RUN == 1, "");
         constexpr int SROWS = WGM * 32, ROW = BN * 4, SBYTES = SROWS * ROW;
-        constexpr int LPR = BN / 8, RPI = 64 / LPR;
         constexpr bool TWICE = 2 * SBYTES <= LDS_BYTES;   // alternate between two halves
         static_assert(SBYTES <= LDS_BYTES, "a stripe fits");
-        constexpr int PER_WAVE = SROWS / NW;
-        static_assert(PER_WAVE % RPI == 0, "whole rows per wave");
-        const int lane = threadIdx.x & 63;
-        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        const int tid = threadIdx.x, lane = tid & 63;
+        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int wm = wave / WGN, wn = wave % WGN;
         typedef __attribute__((address_space(3))) i32x4_t lds_i32x4;
+        typedef __attribute__((address_space(3))) int32_t lds_i32;
         lds_only_barrier();                               // every wave is done with the stages
 #pragma unroll
         for (int i = 0; i < FM; ++i) {
@@ -393,13 +398,22 @@ struct Tile {
                     }
             }
             lds_only_barrier();
+            if constexpr (RUN == 8) {
+                constexpr int LPR = BN / 8;
 #pragma unroll
-            for (int r = 0; r < PER_WAVE; r += RPI) {
-                const int rr = wave * PER_WAVE + r + lane / LPR, c = (lane % LPR) * 2;
-                const i32x4_t lo = *(lds_i32x4 *)(s + rr * ROW + ((c ^ (rr & 15)) << 4));
-                const i32x4_t hi = *(lds_i32x4 *)(s + rr * ROW + (((c + 1) ^ (rr & 15)) << 4));
-                const int v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                f((rr >> 5) * WM + i * 32 + (rr & 31), (lane % LPR) * 8, v);
+                for (int u = 0; u < SROWS * LPR; u += THREADS) {
+                    const int rr = (u + tid) / LPR, c = (tid % LPR) * 2;
+                    const i32x4_t lo = *(lds_i32x4 *)(s + rr * ROW + ((c ^ (rr & 15)) << 4));
+                    const i32x4_t hi = *(lds_i32x4 *)(s + rr * ROW + (((c + 1) ^ (rr & 15)) << 4));
+                    const int v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                    f((rr >> 5) * WM + i * 32 + (rr & 31), (tid % LPR) * 8, v);
+                }
+            } else {
+                for (int u = tid; u < SROWS * BN; u += THREADS) {
+                    const int rr = u / BN, c = u % BN;
+                    const int v[1] = {*(lds_i32 *)(s + rr * ROW + (((c >> 2) ^ (rr & 15)) << 4) + (c & 3) * 4)};
+                    f((rr >> 5) * WM + i * 32 + (rr & 31), c, v);
+                }
             }
         }
     }
