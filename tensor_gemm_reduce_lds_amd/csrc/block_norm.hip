@@ -40,7 +40,7 @@ struct NormArgs {
 };
 
 template <int VEC>
-__device__ __forceinline__ void load_param(const NormArgs &a, const void *p, int64_t i, float add,
+__device__ __forceinline__ void load_param(const NormArgs &a, const void *p, uint32_t i, float add,
                                            float *out) {
     if (a.param_f32) {
         Raw<true, VEC> r;
@@ -64,15 +64,16 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
     int turn = 0;
     const int tid = threadIdx.x;
     const float inv_cols = 1.0f / (float)a.cols;
+    const uint32_t cols = (uint32_t)a.cols;
 
     float w_post[EPT], w_pre[EPT], gate[EPT];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
+        const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
         float *wo = w_post + k * VEC, *wp = w_pre + k * VEC, *g = gate + k * VEC;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) wo[e] = wp[e] = g[e] = 1.0f;
-        if (c < a.cols) {
+        if (c < cols) {
             if (a.post) load_param<VEC>(a, a.w_post, c, a.weight_offset, wo);
             if (a.pre) load_param<VEC>(a, a.w_pre, c, a.weight_offset, wp);
         }
@@ -84,20 +85,20 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
         float x[EPT], y[EPT];
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
+            const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
             xr[k] = Raw<SF, VEC>{};
             yr[k] = Raw<YF, VEC>{};
-            if (c < a.cols) {
-                load_raw(xr[k], a.x, row * a.ld_x + c);
-                if (a.has_y) load_raw(yr[k], a.y, row * a.ld_y + c);
+            if (c < cols) {
+                load_raw(xr[k], row_of(a.x, row, a.ld_x, SF ? 4 : 2), c);
+                if (a.has_y) load_raw(yr[k], row_of(a.y, row, a.ld_y, YF ? 4 : 2), c);
             }
         }
         if (a.gated && row / a.rows_per_gate != gate_row) {
             gate_row = row / a.rows_per_gate;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
-                if (c < a.cols) load_param<VEC>(a, a.gate, gate_row * a.cols + c, 0.0f, gate + k * VEC);
+                const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
+                if (c < cols) load_param<VEC>(a, row_of(a.gate, gate_row, a.cols, a.param_f32 ? 4 : 2), c, 0.0f, gate + k * VEC);
             }
         }
 #pragma unroll
@@ -118,13 +119,13 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
             }
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
+                const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) {
                     const int i = k * VEC + e;
                     x[i] = a.res_scale * x[i] + gate[i] * (y[i] * r2 * w_post[i]);
                 }
-                if (c < a.cols) store_vec<SF, VEC>(a.x_out, row * a.ld_x_out + c, x + k * VEC);
+                if (c < cols) store_vec<SF, VEC>(row_of(a.x_out, row, a.ld_x_out, SF ? 4 : 2), c, x + k * VEC);
             }
         }
         if (!a.pre) continue;
@@ -147,9 +148,9 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
             if (tid == 0) a.u_scale[row] = q.scale;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
-                if (c >= a.cols) continue;
-                int8_t *to = (int8_t *)a.u + row * a.ld_u + c;
+                const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
+                if (c >= cols) continue;
+                int8_t *to = (int8_t *)row_of(a.u, row, a.ld_u, 1) + c;
                 if constexpr (VEC == 8) {
                     u32x2_t w = {0u, 0u};
 #pragma unroll
@@ -163,86 +164,129 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
         } else {
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
-                if (c < a.cols) store_vec<YF, VEC>(a.u, row * a.ld_u + c, x + k * VEC);
+                const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
+                if (c < cols) store_vec<YF, VEC>(row_of(a.u, row, a.ld_u, YF ? 4 : 2), c, x + k * VEC);
             }
         }
     }
 }
 
-template <int VEC, int EPT, int THREADS, bool SF, bool YF>
+// A row's inputs of the backward, as they lie in memory.
+template <int VEC, int VPT, bool SF, bool YF>
+struct BackwardRow {
+    Raw<SF, VEC> x[VPT], d[VPT];
+    Raw<YF, VEC> y[VPT], u[VPT];
+};
+
+template <int VEC, int EPT, int THREADS, bool SF, bool YF, bool AHEAD>
 __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
     constexpr int VPT = EPT / VEC;
+    using Row = BackwardRow<VEC, VPT, SF, YF>;
     __shared__ float slots[2 * 3 * 16];
     int turn = 0;
     const int tid = threadIdx.x;
     const float inv_cols = 1.0f / (float)a.cols;
+    const uint32_t cols = (uint32_t)a.cols;
     const int64_t first = (int64_t)blockIdx.x * a.rows_per_wg;
     int64_t last = first + a.rows_per_wg;
     if (last > a.rows) last = a.rows;
 
-    float w_post[EPT], w_pre[EPT], gate[EPT];
-    float s_post[EPT], s_pre[EPT], s_gate[EPT];
+    // gw: gate * w_post.  Summed over rows: D * yh since the last change of
+    // gate row (dgate is that times w_post, and gate times that goes into
+    // dw_post), and du * xh.
+    float w_pre[EPT], gw[EPT], s_dy[EPT], s_post[EPT], s_pre[EPT];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
-        float *wo = w_post + k * VEC, *wp = w_pre + k * VEC;
+        const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
+        float *wo = gw + k * VEC, *wp = w_pre + k * VEC;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
             const int i = k * VEC + e;
-            wo[e] = wp[e] = gate[i] = 1.0f;
-            s_post[i] = s_pre[i] = s_gate[i] = 0.0f;
+            wo[e] = wp[e] = 1.0f;
+            s_dy[i] = s_post[i] = s_pre[i] = 0.0f;
         }
-        if (c < a.cols) {
+        if (c < cols) {
             if (a.post) load_param<VEC>(a, a.w_post, c, a.weight_offset, wo);
             if (a.pre) load_param<VEC>(a, a.w_pre, c, a.weight_offset, wp);
         }
     }
-    int64_t gate_row = -1;
-    // A gate row's sum: whole if all its rows are this workgroup's, else a
-    // part: the head slot for the group of the first row, the tail slot for
-    // a later one.
-    auto flush_gate = [&](int64_t g) {
-        const int64_t lo = g * a.rows_per_gate;
+    auto take = [&](Row &r, int64_t row) __attribute__((always_inline)) {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
+            r.x[k] = r.d[k] = Raw<SF, VEC>{};
+            r.y[k] = r.u[k] = Raw<YF, VEC>{};
+            if (c < cols && row < last) {
+                if (a.pre) {
+                    load_raw(r.x[k], row_of(a.x_out, row, a.ld_x_out, SF ? 4 : 2), c);
+                    load_raw(r.u[k], row_of(a.du, row, a.ld_du, YF ? 4 : 2), c);
+                }
+                if (a.has_y) load_raw(r.y[k], row_of(a.y, row, a.ld_y, YF ? 4 : 2), c);
+                if (a.dx_out) load_raw(r.d[k], row_of(a.dx_out, row, a.ld_dx_out, SF ? 4 : 2), c);
+            }
+        }
+    };
+    int64_t gate_row = -1, gate_end = first;
+    // Ends a gate row's rows: its part of dw_post, and its dgate, whole if all
+    // its rows are this workgroup's, else a part: the head slot for the gate
+    // row of the first row, the tail slot for a later one.
+    auto end_gate = [&]() __attribute__((always_inline)) {
+        const int64_t lo = gate_row * a.rows_per_gate;
         int64_t hi = lo + a.rows_per_gate;
         if (hi > a.rows) hi = a.rows;
         const bool whole = lo >= first && hi <= last;
-        float *to = whole ? a.dgate + g * a.cols
-                          : a.part + ((int64_t)blockIdx.x * 4 + (g == first / a.rows_per_gate ? 2 : 3)) * a.cols;
+        float *to = whole ? a.dgate + gate_row * a.cols
+                          : a.part + ((int64_t)blockIdx.x * 4 + (gate_row == first / a.rows_per_gate ? 2 : 3)) * a.cols;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
-            if (c < a.cols) store_vec<true, VEC>(to, c, s_gate + k * VEC);
-        }
+            const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
+            if (c >= cols) continue;
+            float g[VEC], w[VEC];
+            load_param<VEC>(a, row_of(a.gate, gate_row, a.cols, a.param_f32 ? 4 : 2), c, 0.0f, g);
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) s_gate[i] = 0.0f;
+            for (int e = 0; e < VEC; ++e) w[e] = 1.0f;
+            if (a.post) load_param<VEC>(a, a.w_post, c, a.weight_offset, w);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+                float &s = s_dy[k * VEC + e];
+                s_post[k * VEC + e] += g[e] * s;
+                w[e] *= s;
+                s = 0.0f;
+            }
+            store_vec<true, VEC>(to, c, w);
+        }
+    };
+    auto begin_gate = [&](int64_t row) __attribute__((always_inline)) {
+        gate_row = row / a.rows_per_gate;
+        gate_end = (gate_row + 1) * a.rows_per_gate;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
+            if (c >= cols) continue;
+            float g[VEC];
+            float *w = gw + k * VEC;
+            load_param<VEC>(a, row_of(a.gate, gate_row, a.cols, a.param_f32 ? 4 : 2), c, 0.0f, g);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) w[e] = 1.0f;
+            if (a.post) load_param<VEC>(a, a.w_post, c, a.weight_offset, w);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) w[e] *= g[e];
+        }
     };
 
+    Row next;
+    if constexpr (AHEAD) take(next, first);
     for (int64_t row = first; row < last; ++row) {
-        Raw<SF, VEC> xr[VPT], dr[VPT];
-        Raw<YF, VEC> yr[VPT], ur[VPT];
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
-            xr[k] = dr[k] = Raw<SF, VEC>{};
-            yr[k] = ur[k] = Raw<YF, VEC>{};
-            if (c < a.cols) {
-                if (a.pre) {
-                    load_raw(xr[k], a.x_out, row * a.ld_x_out + c);
-                    load_raw(ur[k], a.du, row * a.ld_du + c);
-                }
-                if (a.has_y) load_raw(yr[k], a.y, row * a.ld_y + c);
-                if (a.dx_out) load_raw(dr[k], a.dx_out, row * a.ld_dx_out + c);
-            }
+        Row r;
+        if constexpr (AHEAD) {
+            r = next;
+            take(next, row + 1);
+        } else {
+            take(r, row);
         }
-        if (a.gated && row / a.rows_per_gate != gate_row) {
-            if (gate_row >= 0) flush_gate(gate_row);
-            gate_row = row / a.rows_per_gate;
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
-                if (c < a.cols) load_param<VEC>(a, a.gate, gate_row * a.cols + c, 0.0f, gate + k * VEC);
-            }
+        if (a.gated && row >= gate_end) {     // the first row, and each gate row's first
+            if (gate_row >= 0) end_gate();
+            begin_gate(row);
         }
         float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -250,45 +294,37 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 const int i = k * VEC + e;
-                const float x = raw_at(xr[k], e), y = raw_at(yr[k], e);
+                const float x = raw_at(r.x[k], e), y = raw_at(r.y[k], e);
                 s[0] += x * x;
-                s[1] += raw_at(ur[k], e) * w_pre[i] * x;
+                s[1] += raw_at(r.u[k], e) * w_pre[i] * x;
                 s[2] += y * y;
             }
         block_join<Sum, THREADS, 3>(s, slots, turn);
         const float r1 = 1.0f / sqrtf(s[0] * inv_cols + a.eps_pre);
         const float m1 = s[1] * inv_cols * r1;          // mean(a * xh)
         const float r2 = a.post ? 1.0f / sqrtf(s[2] * inv_cols + a.eps_post) : 1.0f;
-        float d[EPT];
+        float b[EPT];
         float t[1] = {0.0f};
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
+            const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
             float dx[VEC];
 #pragma unroll
             for (int e = 0; e < VEC; ++e) {
                 const int i = k * VEC + e;
-                const float xh = raw_at(xr[k], e) * r1, du = raw_at(ur[k], e);
-                d[i] = raw_at(dr[k], e);
-                if (a.pre) d[i] += r1 * (du * w_pre[i] - xh * m1);
+                const float xh = raw_at(r.x[k], e) * r1, du = raw_at(r.u[k], e);
+                float d = raw_at(r.d[k], e);
+                if (a.pre) d += r1 * (du * w_pre[i] - xh * m1);
                 s_pre[i] += du * xh;
-                dx[e] = a.has_y ? a.res_scale * d[i] : d[i];
+                dx[e] = a.has_y ? a.res_scale * d : d;
+                const float yh = raw_at(r.y[k], e) * r2;
+                s_dy[i] += d * yh;
+                b[i] = d * gw[i];
+                t[0] += b[i] * yh;
             }
-            if (c < a.cols) store_vec<SF, VEC>(a.dx, row * a.ld_dx + c, dx);
+            if (c < cols) store_vec<SF, VEC>(row_of(a.dx, row, a.ld_dx, SF ? 4 : 2), c, dx);
         }
         if (!a.has_y) continue;
-#pragma unroll
-        for (int k = 0; k < VPT; ++k)
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const int i = k * VEC + e;
-                const float yh = raw_at(yr[k], e) * r2;
-                s_gate[i] += d[i] * (yh * w_post[i]);
-                d[i] *= gate[i];                         // dz
-                s_post[i] += d[i] * yh;
-                d[i] *= w_post[i];                       // b
-                t[0] += d[i] * yh;
-            }
         float m2 = 0.0f;
         if (a.post) {
             block_join<Sum, THREADS, 1>(t, slots, turn);
@@ -296,20 +332,25 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
         }
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
+            const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
             float dy[VEC];
 #pragma unroll
             for (int e = 0; e < VEC; ++e)
-                dy[e] = r2 * (d[k * VEC + e] - raw_at(yr[k], e) * r2 * m2);
-            if (c < a.cols) store_vec<YF, VEC>(a.dy, row * a.ld_dy + c, dy);
+                dy[e] = r2 * (b[k * VEC + e] - raw_at(r.y[k], e) * r2 * m2);
+            if (c < cols) store_vec<YF, VEC>(row_of(a.dy, row, a.ld_dy, YF ? 4 : 2), c, dy);
         }
     }
-    if (a.gated && gate_row >= 0) flush_gate(gate_row);
+    if (a.gated) {
+        if (gate_row >= 0) end_gate();
+    } else {
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) s_post[i] = s_dy[i];
+    }
     float *part = a.part + (int64_t)blockIdx.x * 4 * a.cols;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        const int64_t c = (int64_t)(k * THREADS + tid) * VEC;
-        if (c >= a.cols) continue;
+        const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
+        if (c >= cols) continue;
         if (a.post) store_vec<true, VEC>(part, c, s_post + k * VEC);
         if (a.pre) store_vec<true, VEC>(part + a.cols, c, s_pre + k * VEC);
     }
@@ -318,13 +359,13 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
 // Adds the workgroups' partial sums.  blockIdx.y: 0 dw_post, 1 dw_pre, then the
 // gate rows whose rows are not all one workgroup's: by gate row (by_group), or
 // by the workgroup w whose end is the first to lie inside the gate row, where
-// that makes fewer workgroups.  64 columns per workgroup; 16 threads per column
-// take every 16th partial, then add up in a fixed order.
+// that makes fewer workgroups.  32 columns per workgroup; 32 threads per column
+// take every 32nd partial, then add up in a fixed order.
 __global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a, int64_t wgs, int by_group,
                                                          float *dw_post, float *dw_pre) {
-    __shared__ float sums[16][64];
-    const int col = threadIdx.x & 63, lane = threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x * 64 + col;
+    __shared__ float sums[32][32];
+    const int col = threadIdx.x & 31, lane = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * 32 + col, cols = a.cols;
     const int y = blockIdx.y;
     float *to = nullptr;
     int64_t lo = 0, hi = wgs, g = -1;
@@ -342,18 +383,20 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(NormArgs a, int64_t wgs
     }
     if (!to) return;
     float s = 0.0f;
-    if (c < a.cols)
+    if (c < cols) {
+        const float *const part = a.part + c;
+        // a gate row's first workgroup has it in its tail slot, unless the
+        // gate row begins with the workgroup's first row
+        const int64_t head_from = g >= 0 ? (g * a.rows_per_gate + a.rows_per_wg - 1) / a.rows_per_wg : 0;
 #pragma unroll 8
-        for (int64_t w = lo + lane; w < hi; w += 16) {
-            int slot = y;
-            if (g >= 0) slot = (w * a.rows_per_wg) / a.rows_per_gate == g ? 2 : 3;
-            s += a.part[(w * 4 + slot) * a.cols + c];
-        }
+        for (int64_t w = lo + lane; w < hi; w += 32)
+            s += part[(w * 4 + (y < 2 ? y : w >= head_from ? 2 : 3)) * cols];
+    }
     sums[lane][col] = s;
     __syncthreads();
-    if (lane == 0 && c < a.cols) {
+    if (lane == 0 && c < cols) {
 #pragma unroll
-        for (int l = 1; l < 16; ++l) s += sums[l][col];
+        for (int l = 1; l < 32; ++l) s += sums[l][col];
         to[c] = s;
     }
 }
@@ -364,18 +407,6 @@ __global__ void norm_zero_kernel(float *a, float *b, int64_t n) {
         if (a) a[i] = 0.0f;
         if (b) b[i] = 0.0f;
     }
-}
-
-// Threads and columns per thread for a row length.
-struct Shape {
-    int threads, ept;
-};
-Shape shape_of(int64_t cols, bool vec) {
-    if (vec && cols <= 512) return {64, 8};
-    if (cols <= 2048) return {256, 8};
-    if (vec && cols <= 4096) return {512, 8};
-    if (cols <= 8192) return {1024, 8};
-    return {1024, 16};
 }
 
 template <int VEC, int EPT, int THREADS>
@@ -401,35 +432,58 @@ void launch_backward(const NormArgs &a, bool sf, bool yf, int64_t grid, hipStrea
     auto go = [&](auto *kernel) {
         hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(THREADS), 0, s, a);
     };
-    if (sf && yf) go(norm_backward_kernel<VEC, EPT, THREADS, true, true>);
-    else if (sf) go(norm_backward_kernel<VEC, EPT, THREADS, true, false>);
-    else if (yf) go(norm_backward_kernel<VEC, EPT, THREADS, false, true>);
-    else go(norm_backward_kernel<VEC, EPT, THREADS, false, false>);
+    constexpr bool AHEAD = VEC == 8 && (EPT == 8 || THREADS < 1024);
+    if (sf && yf) go(norm_backward_kernel<VEC, EPT, THREADS, true, true, AHEAD>);
+    else if (sf) go(norm_backward_kernel<VEC, EPT, THREADS, true, false, AHEAD>);
+    else if (yf) go(norm_backward_kernel<VEC, EPT, THREADS, false, true, AHEAD>);
+    else go(norm_backward_kernel<VEC, EPT, THREADS, false, false, AHEAD>);
 }
 
-// Calls f with the kernel shape's constants.
+// Threads of a workgroup and columns of a row per thread.
+template <int VEC_, int EPT_, int THREADS_>
+struct Shape {
+    static constexpr int VEC = VEC_, EPT = EPT_, THREADS = THREADS_;
+};
+
+// Calls f with the kernel shape of a row length.
 template <class F>
-void with_shape(int64_t cols, bool vec, F f) {
-    const Shape sh = shape_of(cols, vec);
+void forward_shape(int64_t cols, bool vec, F f) {
     if (vec) {
-        if (sh.threads == 64) f(std::integral_constant<int, 8>{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 64>{});
-        else if (sh.threads == 256) f(std::integral_constant<int, 8>{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 256>{});
-        else if (sh.threads == 512) f(std::integral_constant<int, 8>{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 512>{});
-        else if (sh.ept == 8) f(std::integral_constant<int, 8>{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 1024>{});
-        else f(std::integral_constant<int, 8>{}, std::integral_constant<int, 16>{}, std::integral_constant<int, 1024>{});
+        if (cols <= 512) f(Shape<8, 8, 64>{});
+        else if (cols <= 2048) f(Shape<8, 8, 256>{});
+        else if (cols <= 4096) f(Shape<8, 8, 512>{});
+        else if (cols <= 8192) f(Shape<8, 8, 1024>{});
+        else f(Shape<8, 16, 1024>{});
     } else {
-        if (sh.threads == 256) f(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 256>{});
-        else if (sh.ept == 8) f(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 1024>{});
-        else f(std::integral_constant<int, 1>{}, std::integral_constant<int, 16>{}, std::integral_constant<int, 1024>{});
+        if (cols <= 2048) f(Shape<1, 8, 256>{});
+        else if (cols <= 8192) f(Shape<1, 8, 1024>{});
+        else f(Shape<1, 16, 1024>{});
+    }
+}
+template <class F>
+void backward_shape(int64_t cols, bool vec, F f) {
+    if (vec) {
+        if (cols <= 512) f(Shape<8, 8, 64>{});
+        else if (cols <= 2048) f(Shape<8, 8, 256>{});
+        else if (cols <= 4096) f(Shape<8, 8, 512>{});
+        else if (cols <= 8192) f(Shape<8, 16, 512>{});
+        else f(Shape<8, 16, 1024>{});
+    } else {
+        if (cols <= 2048) f(Shape<1, 8, 256>{});
+        else if (cols <= 8192) f(Shape<1, 16, 512>{});
+        else f(Shape<1, 16, 1024>{});
     }
 }
 
 // Most workgroups of a backward launch: enough to fill the CUs' wave slots
-// that the kernel's registers allow (16 waves per CU), and no more, because
-// each writes 4 rows of partial sums.
+// that the kernel's registers allow, and no more, because each writes 4 rows
+// of partial sums.
 int64_t backward_wgs(int64_t rows, int64_t cols, bool vec) {
-    const int64_t most = (int64_t)kCus * 1024 / shape_of(cols, vec).threads;
-    const int64_t cap = most < 2048 ? most : 2048;
+    int64_t cap = 0;
+    backward_shape(cols, vec, [&](auto sh) {
+        cap = (int64_t)kCus * 512 / decltype(sh)::THREADS;
+    });
+    if (cap > 2048) cap = 2048;
     return rows < cap ? rows : cap;
 }
 
@@ -561,9 +615,10 @@ int block_norm_run(block_norm_plan_t p, const void *x, const void *y, const void
     const bool vec = d.cols % 8 == 0 && wide(x, a.ld_x, se) && wide(y, a.ld_y, ye) &&
                      wide(w_post, 8, pe) && wide(gate, 8, pe) && wide(w_pre, 8, pe) &&
                      wide(x_out, a.ld_x_out, se) && wide(u, a.ld_u, ue);
-    with_shape(d.cols, vec, [&](auto v, auto ept, auto threads) {
-        const int64_t most = (int64_t)kCus * 2048 / threads.value;
-        launch_forward<v.value, ept.value, threads.value>(
+    forward_shape(d.cols, vec, [&](auto sh) {
+        using S = decltype(sh);
+        const int64_t most = (int64_t)kCus * 2048 / S::THREADS;
+        launch_forward<S::VEC, S::EPT, S::THREADS>(
             a, d.stream_dtype == GEMM_RS_F32, d.dtype == GEMM_RS_F32, d.quant != 0,
             rows < most ? rows : most, (hipStream_t)stream);
     });
@@ -610,8 +665,9 @@ int block_norm_backward(block_norm_plan_t p, const void *dx_out, const void *du,
     int64_t wgs = backward_wgs(rows, d.cols, vec);
     a.rows_per_wg = (rows + wgs - 1) / wgs;
     wgs = (rows + a.rows_per_wg - 1) / a.rows_per_wg;
-    with_shape(d.cols, vec, [&](auto v, auto ept, auto threads) {
-        launch_backward<v.value, ept.value, threads.value>(
+    backward_shape(d.cols, vec, [&](auto sh) {
+        using S = decltype(sh);
+        launch_backward<S::VEC, S::EPT, S::THREADS>(
             a, d.stream_dtype == GEMM_RS_F32, d.dtype == GEMM_RS_F32, wgs, s);
     });
     if (hipGetLastError() != hipSuccess) return GEMM_RS_ERR_HIP;
@@ -621,7 +677,7 @@ int block_norm_backward(block_norm_plan_t p, const void *dx_out, const void *du,
         const int64_t gates = (rows + a.rows_per_gate - 1) / a.rows_per_gate;
         const bool by_group = gates < wgs - 1;
         const unsigned ny = 2 + (split ? (unsigned)(by_group ? gates : wgs - 1) : 0);
-        hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)((d.cols + 63) / 64), ny), dim3(1024), 0, s,
+        hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)((d.cols + 31) / 32), ny), dim3(1024), 0, s,
                            a, wgs, (int)by_group, (float *)dw_post, (float *)dw_pre);
     }
     return hipGetLastError() == hipSuccess ? GEMM_RS_OK : GEMM_RS_ERR_HIP;

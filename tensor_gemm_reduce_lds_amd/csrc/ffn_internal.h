@@ -47,8 +47,17 @@ template <> struct Raw<false, 8> { u32x4_t a; };
 template <> struct Raw<true, 1> { float a; };
 template <> struct Raw<false, 1> { uint16_t a; };
 
+// Row `row` of a matrix of `elem`-byte elements: a wave-uniform address, which
+// a 32-bit column number per lane is added to.
+__device__ __forceinline__ const void *row_of(const void *p, int64_t row, int64_t ld, int elem) {
+    return (const char *)p + row * ld * elem;
+}
+__device__ __forceinline__ void *row_of(void *p, int64_t row, int64_t ld, int elem) {
+    return (char *)p + row * ld * elem;
+}
+
 template <bool F32, int VEC>
-__device__ __forceinline__ void load_raw(Raw<F32, VEC> &r, const void *p, int64_t i) {
+__device__ __forceinline__ void load_raw(Raw<F32, VEC> &r, const void *p, uint32_t i) {
     if constexpr (VEC == 8 && F32) {
         const u32x4_t *q = (const u32x4_t *)((const float *)p + i);
         r.a = q[0];
@@ -75,7 +84,7 @@ __device__ __forceinline__ float raw_at(const Raw<F32, VEC> &r, int e) {
 }
 
 template <bool F32, int VEC>
-__device__ __forceinline__ void store_vec(void *p, int64_t i, const float *v) {
+__device__ __forceinline__ void store_vec(void *p, uint32_t i, const float *v) {
     if constexpr (VEC == 8 && F32) {
         f32x4_t *q = (f32x4_t *)((float *)p + i);
         q[0] = f32x4_t{v[0], v[1], v[2], v[3]};

@@ -197,23 +197,24 @@ __device__ __forceinline__ void store8(const GroupedArgs &p, int64_t row, int64_
     float x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = __int_as_float(v[e]);
-    const int64_t at = row * p.ldc + n;
+    const uint32_t at = (uint32_t)n;
+    void *const C = row_of(p.C, row, p.ldc, p.out_f32 ? 4 : 2);
     if (p.out_f32) {
         if (p.accumulate) {
             Raw<true, 8> c;
-            load_raw(c, p.C, at);
+            load_raw(c, C, at);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] += raw_at(c, e);
         }
-        store_vec<true, 8>(p.C, at, x);
+        store_vec<true, 8>(C, at, x);
     } else {
         if (p.accumulate) {
             Raw<false, 8> c;
-            load_raw(c, p.C, at);
+            load_raw(c, C, at);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] += raw_at(c, e);
         }
-        store_vec<false, 8>(p.C, at, x);
+        store_vec<false, 8>(C, at, x);
     }
 }
 

@@ -65,8 +65,8 @@ __global__ __launch_bounds__(64 * WGM * WGN) void q8_tile_kernel(Q8Args p) {
             float x[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = scaled(v[e], sa, sw[e], p.bias ? &bias[e] : nullptr);
-            if (p.out_f32) store_vec<true, 8>(p.D, m * p.ldd + n0 + c, x);
-            else store_vec<false, 8>(p.D, m * p.ldd + n0 + c, x);
+            if (p.out_f32) store_vec<true, 8>(row_of(p.D, m, p.ldd, 4), (uint32_t)(n0 + c), x);
+            else store_vec<false, 8>(row_of(p.D, m, p.ldd, 2), (uint32_t)(n0 + c), x);
         });
     } else {
         tile.template store<1>(smem, [&](int r, int c, const int (&v)[1]) {
@@ -212,7 +212,7 @@ __global__ __launch_bounds__(THREADS) void quantize_kernel(const void *x, int64_
         float m[1] = {0.0f};
         auto take = [&](Raw<F32, VEC> &r, int64_t c) {
             r = Raw<F32, VEC>{};
-            if (c < cols) load_raw(r, x, row * ldx + c);
+            if (c < cols) load_raw(r, row_of(x, row, ldx, F32 ? 4 : 2), (uint32_t)c);
         };
         auto look = [&](const Raw<F32, VEC> &r) {
 #pragma unroll
