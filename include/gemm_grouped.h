@@ -84,6 +84,7 @@ GEMM_RS_API int gemm_grouped_plan(const gemm_grouped_desc_t *desc, gemm_grouped_
  *   offsets  int32 [E+1] on the device, non-decreasing, within 0..rows.
  *            Other values are clipped to that (no access leaves the
  *            arrays) and reported by gemm_grouped_status.
+ * One plan of TN must not run on two streams at once (its workspace).
  * Returns OK, INVALID_ARG (NULL or misaligned pointers, rows out of range,
  * another device) or HIP.
  */

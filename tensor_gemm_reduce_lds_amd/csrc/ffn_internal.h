@@ -83,19 +83,27 @@ __device__ __forceinline__ float raw_at(const Raw<F32, VEC> &r, int e) {
         return bf16_lo(r.a);
 }
 
-template <bool F32, int VEC>
+template <bool F32, int VEC, bool STREAM = false>
 __device__ __forceinline__ void store_vec(void *p, uint32_t i, const float *v) {
     if constexpr (VEC == 8 && F32) {
         f32x4_t *q = (f32x4_t *)((float *)p + i);
-        q[0] = f32x4_t{v[0], v[1], v[2], v[3]};
-        q[1] = f32x4_t{v[4], v[5], v[6], v[7]};
+        const f32x4_t a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
+        if constexpr (STREAM) {
+            __builtin_nontemporal_store(a, q);
+            __builtin_nontemporal_store(b, q + 1);
+        } else {
+            q[0] = a;
+            q[1] = b;
+        }
     } else if constexpr (VEC == 8) {
         u32x4_t w;
         w[0] = pack_bf16(v[0], v[1]);
         w[1] = pack_bf16(v[2], v[3]);
         w[2] = pack_bf16(v[4], v[5]);
         w[3] = pack_bf16(v[6], v[7]);
-        *(u32x4_t *)((uint16_t *)p + i) = w;
+        u32x4_t *q = (u32x4_t *)((uint16_t *)p + i);
+        if constexpr (STREAM) __builtin_nontemporal_store(w, q);
+        else *q = w;
     } else if constexpr (F32) {
         ((float *)p)[i] = v[0];
     } else {

@@ -4,6 +4,7 @@
 // workgroups that any split of the rows over the experts can need (one
 // partly filled row tile per expert) and each workgroup finds its tile from
 // the offsets.
+#include <math.h>
 #include <stdlib.h>
 
 #include "gemm_grouped.h"
@@ -24,6 +25,8 @@ struct GroupedArgs {
     const int32_t *offsets;
     void *C;
     int32_t *err;
+    int32_t parts;                // TN: workgroups that share a tile's contraction
+    float *slots;                 // their sums, [part][E][K][N] (parts > 1)
 };
 
 // Rows [lo, hi) of expert e, clipped to 0 <= lo <= hi <= rows.
@@ -192,7 +195,10 @@ __global__ __launch_bounds__(256) void grouped_narrow_kernel(GroupedArgs p) {
     }
 }
 
-// 8 columns of a row of C.
+// 8 columns of a row of C.  STREAM: a weight gradient, many times the caches'
+// size, is stored past them (6001 rows, 32 experts of 2048 x 1792 in 32 bits:
+// 165 us, streamed 129).
+template <bool STREAM>
 __device__ __forceinline__ void store8(const GroupedArgs &p, int64_t row, int64_t n, const int (&v)[8]) {
     float x[8];
 #pragma unroll
@@ -206,7 +212,7 @@ __device__ __forceinline__ void store8(const GroupedArgs &p, int64_t row, int64_
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] += raw_at(c, e);
         }
-        store_vec<true, 8>(C, at, x);
+        store_vec<true, 8, STREAM>(C, at, x);
     } else {
         if (p.accumulate) {
             Raw<false, 8> c;
@@ -214,13 +220,25 @@ __device__ __forceinline__ void store8(const GroupedArgs &p, int64_t row, int64_
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] += raw_at(c, e);
         }
-        store_vec<false, 8>(C, at, x);
+        store_vec<false, 8, STREAM>(C, at, x);
     }
 }
 
 // Sizes, strides and addresses that are multiples of 8 elements.
 template <int OP, int BM, int BN, int WGM, int WGN, int STAGES>
 using GroupedTile = Tile<f32x16_t, BM, BN, WGM, WGN, OP == GEMM_GROUPED_TN, OP != GEMM_GROUPED_NT, STAGES>;
+
+// A from the tile's first row, and expert e's B from column n0 (NN, NT).
+__device__ __forceinline__ Operand row_operand(const GroupedArgs &p, const RowTile &t, int32_t rows) {
+    return {(const char *)(p.A + (int64_t)t.row0 * p.lda), p.lda * 2, rows};
+}
+template <int OP>
+__device__ __forceinline__ Operand column_operand(const GroupedArgs &p, int e, int64_t n0, int32_t cols) {
+    if constexpr (OP == GEMM_GROUPED_NN)
+        return {(const char *)(p.B + (int64_t)e * p.K * p.ldb + n0), p.ldb * 2, cols * 2};
+    else
+        return {(const char *)(p.B + ((int64_t)e * p.N + n0) * p.ldb), p.ldb * 2, cols};
+}
 
 template <int OP, int BM, int BN, int WGM, int WGN, int STAGES>
 __global__ __launch_bounds__(64 * WGM * WGN) void grouped_tile_kernel(GroupedArgs p) {
@@ -232,23 +250,35 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_tile_kernel(GroupedArg
     if constexpr (OP == GEMM_GROUPED_TN) {
         // XCD x takes the x-th eighth of every expert's tiles, so the XCDs'
         // shares are equal however uneven the groups are
-        const int tiles = p.tiles_m * p.tiles_n, per = (tiles + 7) / 8;
+        const int tiles = p.tiles_m * p.tiles_n * p.parts, per = (tiles + 7) / 8;
         const int j = blockIdx.x / 8, e = j / per;
-        const int t = (int)(blockIdx.x % 8) * per + (j - e * per);
-        if (t >= tiles) return;
+        const int u = (int)(blockIdx.x % 8) * per + (j - e * per);
+        if (u >= tiles) return;
+        const int t = u / p.parts, part = u - t * p.parts;
         const int64_t m0 = (int64_t)(t / p.tiles_n) * BM, n0 = (int64_t)(t % p.tiles_n) * BN;
         int32_t lo, hi;
         group_rows(p, e, &lo, &hi);
         lo = __builtin_amdgcn_readfirstlane(lo);
         hi = __builtin_amdgcn_readfirstlane(hi);
-        if (hi == lo && p.accumulate) return;
+        if (hi == lo && p.accumulate && p.parts == 1) return;
         const int32_t m_left = (int32_t)(p.K - m0 < BM ? p.K - m0 : BM);
         const int32_t n_left = (int32_t)(p.N - n0 < BN ? p.N - n0 : BN);
+        GroupedArgs out = p;
+        if (p.parts > 1) {
+            const uint32_t steps = (uint32_t)T::template steps_of<2>(hi - lo);
+            const int32_t end = lo + (int32_t)((uint64_t)(part + 1) * steps / p.parts) * 64;
+            lo += (int32_t)((uint64_t)part * steps / p.parts) * 64;
+            hi = hi < end ? hi : end;
+            out.C = p.slots + (int64_t)part * p.E * p.K * p.N;
+            out.ldc = p.N;
+            out.out_f32 = 1;
+            out.accumulate = 0;
+        }
         const Operand a = {(const char *)(p.A + (int64_t)lo * p.lda + m0), p.lda * 2, m_left * 2};
         const Operand b = {(const char *)(p.B + (int64_t)lo * p.ldb + n0), p.ldb * 2, n_left * 2};
         tile.template run<2>(smem, a, b, hi - lo);
         tile.template store<8>(smem, [&](int r, int c, const int (&v)[8]) {
-            if (r < m_left && c < n_left) store8(p, (int64_t)e * p.K + m0 + r, n0 + c, v);
+            if (r < m_left && c < n_left) store8<true>(out, (int64_t)e * p.K + m0 + r, n0 + c, v);
         });
     } else {
         RowTile t;
@@ -256,15 +286,162 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_tile_kernel(GroupedArg
         const int64_t n0 = (int64_t)t.tn * BN;
         const int32_t m_left = t.hi - t.row0 < BM ? t.hi - t.row0 : BM;
         const int32_t n_left = (int32_t)(p.N - n0 < BN ? p.N - n0 : BN);
-        const Operand a = {(const char *)(p.A + (int64_t)t.row0 * p.lda), p.lda * 2, m_left};
-        const Operand b = OP == GEMM_GROUPED_NN
-            ? Operand{(const char *)(p.B + (int64_t)t.e * p.K * p.ldb + n0), p.ldb * 2, n_left * 2}
-            : Operand{(const char *)(p.B + ((int64_t)t.e * p.N + n0) * p.ldb), p.ldb * 2, n_left};
-        tile.template run<2>(smem, a, b, (int32_t)p.K);
+        tile.template run<2>(smem, row_operand(p, t, m_left), column_operand<OP>(p, t.e, n0, n_left), (int32_t)p.K);
         tile.template store<8>(smem, [&](int r, int c, const int (&v)[8]) {
-            if (r < m_left && c < n_left) store8(p, (int64_t)t.row0 + r, n0 + c, v);
+            if (r < m_left && c < n_left) store8<false>(p, (int64_t)t.row0 + r, n0 + c, v);
         });
     }
+}
+
+// Few rows per expert (NN, NT): MB * 32 rows and BN columns per workgroup.
+// Bound by streaming B, so the contraction is dealt out to the NW waves 64 at
+// a time and each wave streams its share through S stages of LDS of its own:
+// no wave waits for another until their sums meet, in the order of the waves.
+template <int OP, int MB, int BN, int NW, int S>
+struct StreamTile {
+    static constexpr int BM = MB * 32, FN = BN / 32;
+    static constexpr int A_LOADS = MB * 4, B_LOADS = BN / 8, LOADS = A_LOADS + B_LOADS;   // of 1 KB
+    static constexpr int A_BYTES = A_LOADS * 1024, STAGE = LOADS * 1024;
+    static constexpr int THREADS = NW * 64, LDS_BYTES = NW * S * STAGE;
+    static constexpr bool COL = OP == GEMM_GROUPED_NN;
+    static_assert(BN == 64, "B's rows of a stage are 128 bytes in both forms");
+    static_assert(LDS_BYTES <= 160 * 1024 && BM * BN * 4 <= S * STAGE, "LDS");
+    static_assert((S - 1) * LOADS < 64, "the load counter");
+
+    // 16-byte chunk c of row r of a stage's tile sits at c ^ swz.  B in NN (r: a
+    // row of the contraction): a transposing read takes 4 rows of 4 chunks.
+    static __device__ __forceinline__ int row_swz(int r) { return (r ^ (r >> 3)) & 7; }
+    static __device__ __forceinline__ int col_swz(int r) { return 4 * ((r >> 1) & 1); }
+
+    template <class F>
+    static __device__ __forceinline__ void run(lds_t *smem, const Operand &a, const Operand &b, int32_t K, F store) {
+        const int tid = threadIdx.x, lane = tid & 63;
+        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int pieces = (int)(((uint32_t)K + 63) / 64);
+        const int mine = pieces > wave ? (pieces - wave + NW - 1) / NW : 0;
+        lds_t *const own = smem + wave * (S * STAGE);
+        const uint32_t own_base = (uint32_t)(size_t)own;
+        const int lr = lane >> 3, lc = lane & 7;
+        // a lane's offset in load i: rows i * 8 + lr; the row swizzle takes 8
+        // values over i, the column swizzle one
+        auto issue = [&](int piece, int st) __attribute__((always_inline)) {
+            const int k = (piece * NW + wave) * 64;
+            const int left = K - k < 64 ? K - k : 64;
+            const i32x4_t ra = buffer_of(a.base + (int64_t)k * 2, (uint32_t)(a.span - 1) * (uint32_t)a.ld + left * 2);
+            const i32x4_t rb = COL ? buffer_of(b.base + (int64_t)k * b.ld, (uint32_t)(left - 1) * (uint32_t)b.ld + (uint32_t)b.span)
+                                   : buffer_of(b.base + (int64_t)k * 2, (uint32_t)(b.span - 1) * (uint32_t)b.ld + left * 2);
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) {
+                const bool isb = i >= A_LOADS;
+                const int r = (isb ? i - A_LOADS : i) * 8 + lr;
+                const int c = lc ^ (isb && COL ? col_swz(r) : row_swz(r));
+                uint32_t v = (uint32_t)r * (uint32_t)(isb ? b.ld : a.ld) + c * 16;
+                // past the contraction's end: rows of NN's B lie past the
+                // descriptor, chunks of the others are sent there
+                if (!(isb && COL) && c * 8 >= left) v = 0xfffffff0u;
+                load_to_lds(isb ? rb : ra, v, own_base + st * STAGE + i * 1024);
+            }
+        };
+        typedef __attribute__((address_space(3))) i32x4_t lds_i32x4;
+        typedef __attribute__((address_space(3))) i16x4_t lds_i16x4;
+        typedef __attribute__((address_space(3))) f32x4_t lds_f32x4;
+        f32x16_t acc[MB][FN];
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j) acc[i][j] = f32x16_t{};
+        const int grp = lane >> 4, te = (lane & 15) >> 2, tq = lane & 3;
+#pragma unroll
+        for (int s = 0; s < S - 1; ++s)
+            if (s < mine) issue(s, s);
+        int st = 0;
+        for (int n = 0; n < mine; ++n) {
+            wait_groups<LOADS, S - 2>(mine - 1 - n);
+            if (n + S - 1 < mine) issue(n + S - 1, st == 0 ? S - 1 : st - 1);
+            lds_t *const at = own + st * STAGE, *const bt = at + A_BYTES;
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                i32x4_t af[MB], bf[FN];
+#pragma unroll
+                for (int i = 0; i < MB; ++i) {
+                    const int r = i * 32 + (lane & 31);
+                    af[i] = *(lds_i32x4 *)(at + r * 128 + (((2 * ks + (lane >> 5)) ^ row_swz(r)) << 4));
+                }
+#pragma unroll
+                for (int j = 0; j < FN; ++j) {
+                    if constexpr (COL) {
+                        const int r = ks * 16 + 8 * (grp >> 1) + te, x = j * 32 + 16 * (grp & 1) + 4 * tq;
+                        // rows r and r + 4 have the same swizzle
+                        lds_t *const q = bt + r * 128 + (((x >> 3) ^ col_swz(r)) << 4) + ((x & 7) << 1);
+                        const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)q);
+                        const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(q + 4 * 128));
+                        bf[j] = __builtin_bit_cast(i32x4_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+                    } else {
+                        const int r = j * 32 + (lane & 31);
+                        bf[j] = *(lds_i32x4 *)(bt + r * 128 + (((2 * ks + (lane >> 5)) ^ row_swz(r)) << 4));
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < MB; ++i)
+#pragma unroll
+                    for (int j = 0; j < FN; ++j) acc[i][j] = mma(af[i], bf[j], acc[i][j]);
+            }
+            // the reads are done before the next issue overwrites their stage
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            if (++st == S) st = 0;
+        }
+#pragma unroll
+        for (int i = 0; i < MB; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const f32x4_t v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+                    *(lds_f32x4 *)(own + ((i * 32 + (lane & 31)) * BN + j * 32 + 8 * q + 4 * (lane >> 5)) * 4) = v;
+                }
+        __syncthreads();
+        for (int u = tid; u < BM * BN / 8; u += THREADS) {
+            const int r = u / (BN / 8), c = u % (BN / 8) * 8;
+            f32x4_t lo = {0, 0, 0, 0}, hi = {0, 0, 0, 0};
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                lds_t *const q = smem + w * (S * STAGE) + (r * BN + c) * 4;
+                lo += *(lds_f32x4 *)q;
+                hi += *(lds_f32x4 *)(q + 16);
+            }
+            int v[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                v[e] = __float_as_int(lo[e]);
+                v[e + 4] = __float_as_int(hi[e]);
+            }
+            store(r, c, v);
+        }
+    }
+};
+
+template <int OP, int MB, int BN, int NW, int S>
+__global__ __launch_bounds__(NW * 64) void grouped_stream_kernel(GroupedArgs p) {
+    using T = StreamTile<OP, MB, BN, NW, S>;
+    extern __shared__ __attribute__((aligned(1024))) char smem_generic[];
+    if (blockIdx.x == 0 && threadIdx.x < 64) check_offsets(p);
+    RowTile t;
+    if (!find_row_tile(p, T::BM, blockIdx.x, &t)) return;
+    const int64_t n0 = (int64_t)t.tn * BN;
+    const int32_t m_left = t.hi - t.row0 < T::BM ? t.hi - t.row0 : T::BM;
+    const int32_t n_left = (int32_t)(p.N - n0 < BN ? p.N - n0 : BN);
+    T::run((lds_t *)smem_generic, row_operand(p, t, m_left), column_operand<OP>(p, t.e, n0, n_left),
+           (int32_t)p.K, [&](int r, int c, const int (&v)[8]) {
+               if (r < m_left && c < n_left) store8<false>(p, (int64_t)t.row0 + r, n0 + c, v);
+           });
+}
+
+template <int OP, int MB, int BN, int NW, int S>
+hipError_t launch_stream(GroupedArgs &a, hipStream_t s) {
+    using T = StreamTile<OP, MB, BN, NW, S>;
+    a.tiles_n = (int32_t)((a.N + BN - 1) / BN);
+    const int64_t blocks = (a.rows / T::BM + (a.E < a.rows ? a.E : a.rows)) * a.tiles_n;
+    return launch_lds<grouped_stream_kernel<OP, MB, BN, NW, S>>(blocks, T::THREADS, T::LDS_BYTES, s, a);
 }
 
 template <int OP, int BM, int BN, int WGM, int WGN, int STAGES>
@@ -273,9 +450,106 @@ hipError_t launch_tile(GroupedArgs &a, hipStream_t s) {
     a.tiles_n = (int32_t)((a.N + BN - 1) / BN);
     a.tiles_m = (int32_t)((a.K + BM - 1) / BM);
     int64_t blocks;
-    if (OP == GEMM_GROUPED_TN) blocks = (((int64_t)a.tiles_m * a.tiles_n + 7) / 8) * 8 * a.E;
+    if (OP == GEMM_GROUPED_TN) blocks = (((int64_t)a.tiles_m * a.tiles_n * a.parts + 7) / 8) * 8 * a.E;
     else blocks = (a.rows / BM + (a.E < a.rows ? a.E : a.rows)) * a.tiles_n;
     return launch_lds<grouped_tile_kernel<OP, BM, BN, WGM, WGN, STAGES>>(blocks, T::THREADS, T::LDS_BYTES, s, a);
+}
+
+// Adds the parts of every weight gradient, in their order.
+__global__ __launch_bounds__(256) void grouped_join_kernel(GroupedArgs p) {
+    const int64_t runs = p.N / 8, all = (int64_t)p.E * p.K * runs;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
+        const int64_t row = i / runs, n = i % runs * 8;
+        float x[8] = {};
+        for (int s = 0; s < p.parts; ++s) {
+            Raw<true, 8> r;
+            load_raw(r, p.slots + ((int64_t)s * p.E * p.K + row) * p.N, (uint32_t)n);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] += raw_at(r, e);
+        }
+        int v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = __float_as_int(x[e]);
+        store8<false>(p, row, n, v);
+    }
+}
+
+double ceil_div(double a, double b) { return ceil(a / b); }
+
+// Row tiles of bm rows, as far as the host can tell: every expert with rows
+// has one that is half empty.
+double row_tiles(const GroupedArgs &a, int bm) {
+    const double live = a.E < a.rows ? a.E : a.rows;
+    const double t = (double)a.rows / bm + live / 2;
+    return t > live ? t : live;
+}
+
+// NN and NT: the tile with the least time, rounds of 256 workgroups times the
+// steps of 64 times a step's time (us, measured; a round costs about as much
+// where it is not full), but not less than the operands take from memory.
+// Large tiles do the most work per byte, small ones fill the CUs; of equals the
+// larger, which reads B less often where an expert has more rows than the mean.
+// Measured, us for 256 x 256, 128 x 256, 128 x 128, 64 x 64 and 32 x 64 streams
+// (rows : N : K : E): 16384 : 3584 : 4096 : 8 453, 524, 633, -, -;
+// 8000 : 1792 : 4096 : 64 256, 221, 253, -, -; 512 : 3584 : 4096 : 8 104, 64, 50,
+// 79, 92; 128 : 1024 : 2048 : 1 -, -, 20, 11, 8.4; 32 : 3584 : 4096 : 1 -, -, 35,
+// 18, 16.
+template <int OP>
+hipError_t launch_rows(GroupedArgs &a, hipStream_t s) {
+    struct Option {
+        int bm, bn;
+        double step;
+    };
+    const Option options[] = {{256, 256, 1.77}, {128, 256, 1.02}, {128, 128, 0.66}, {64, 64, 0.34}, {32, 64, 0.25}};
+    const double live = a.E < a.rows ? a.E : a.rows, steps = ceil_div((double)a.K, 64);
+    const double floor_us = 2.0 * (live * a.K * a.N + (double)a.rows * (a.K + a.N)) / 5.0e6;
+    int best = 0;
+    double best_us = 0;
+    for (int i = 0; i < 5; ++i) {
+        const Option &o = options[i];
+        double us = ceil_div(row_tiles(a, o.bm) * ceil_div((double)a.N, o.bn), kCus) * steps * o.step;
+        if (us < floor_us) us = floor_us;
+        if (i == 0 || us < 0.97 * best_us) {
+            best = i;
+            best_us = us;
+        }
+    }
+    switch (best) {
+    case 0: return launch_tile<OP, 256, 256, 2, 4, 2>(a, s);
+    case 1: return launch_tile<OP, 128, 256, 2, 4, 3>(a, s);
+    case 2: return launch_tile<OP, 128, 128, 2, 4, 4>(a, s);
+    case 3: return launch_stream<OP, 2, 64, 4, 2>(a, s);
+    default: return launch_stream<OP, 1, 64, 4, 3>(a, s);
+    }
+}
+
+// TN: 256 x 256 tiles, or 128 x 128 with two workgroups per CU, so that one
+// stores while the other loads: better for short groups, whose time is the
+// stores (us for 256 / 128: 188 rows per expert 158 / 129, 2048 rows 440 / 564),
+// and where there are fewer large tiles than CUs.  With few of the small ones
+// too, `parts` workgroups share a tile's rows and a second kernel adds them.
+struct TnChoice {
+    bool large;
+    int parts;
+};
+TnChoice tn_choice(int64_t rows, int64_t K, int64_t N, int64_t E) {
+    const int64_t large = E * ((K + 255) / 256) * ((N + 255) / 256);
+    const int64_t small = E * ((K + 127) / 128) * ((N + 127) / 128);
+    const int64_t steps = rows / E / 64;
+    if (large >= kCus && rows / E >= 448) return {true, 1};
+    int64_t parts = 2 * kCus / small < steps / 4 ? 2 * kCus / small : steps / 4;
+    if (parts > 16) parts = 16;
+    return {false, (int)(parts < 2 ? 1 : parts)};
+}
+hipError_t launch_tn(GroupedArgs &a, hipStream_t s) {
+    const TnChoice c = tn_choice(a.rows, a.K, a.N, a.E);
+    if (c.large) return launch_tile<GEMM_GROUPED_TN, 256, 256, 2, 4, 2>(a, s);
+    a.parts = c.parts;
+    hipError_t e = launch_tile<GEMM_GROUPED_TN, 128, 128, 2, 2, 2>(a, s);
+    if (e != hipSuccess || c.parts == 1) return e;
+    const int64_t blocks = ((int64_t)a.E * a.K * (a.N / 8) + 255) / 256;
+    hipLaunchKernelGGL(grouped_join_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s, a);
+    return hipGetLastError();
 }
 
 template <int OP>
@@ -288,16 +562,15 @@ hipError_t launch_op(GroupedArgs &a, bool wide, hipStream_t s) {
         hipLaunchKernelGGL(grouped_narrow_kernel<OP>, dim3((unsigned)(row_tiles * a.tiles_n)), dim3(256), 0, s, a);
         return hipGetLastError();
     }
-    if constexpr (OP == GEMM_GROUPED_TN) {
-        const int64_t big = (int64_t)a.E * ((a.K + 255) / 256) * ((a.N + 255) / 256);
-        if (big >= kCus) return launch_tile<OP, 256, 256, 2, 4, 2>(a, s);
-        return launch_tile<OP, 128, 128, 2, 2, 4>(a, s);
-    } else {
-        const int64_t avg = a.rows / a.E;      // the sizes themselves are on the device
-        if (avg >= 192) return launch_tile<OP, 256, 256, 2, 4, 2>(a, s);
-        if (avg >= 48) return launch_tile<OP, 128, 128, 2, 2, 4>(a, s);
-        return launch_tile<OP, 32, 128, 1, 4, 6>(a, s);
-    }
+    if constexpr (OP == GEMM_GROUPED_TN) return launch_tn(a, s);
+    else return launch_rows<OP>(a, s);
+}
+
+// Bytes of the parts of any call of a plan.
+int64_t slot_bytes(const gemm_grouped_desc_t &d) {
+    if (d.op != GEMM_GROUPED_TN || d.N % 8 != 0 || d.K % 8 != 0) return 0;
+    const int64_t parts = tn_choice(d.M, d.K, d.N, d.E).parts;   // most for the most rows
+    return parts > 1 ? parts * d.E * d.K * d.N * (int64_t)sizeof(float) : 0;
 }
 
 int validate(const gemm_grouped_desc_t &d) {
@@ -327,6 +600,8 @@ struct gemm_grouped_plan_s {
     gemm_grouped_desc_t d;    // strides filled in
     int device;
     int32_t *err;
+    float *slots;        // parts of weight gradients (tn_choice), or null
+    int64_t slot_bytes;
 };
 
 extern "C" {
@@ -344,11 +619,14 @@ int gemm_grouped_plan(const gemm_grouped_desc_t *desc, gemm_grouped_plan_t *out)
     if (!p->d.ldc) p->d.ldc = p->d.N;
     hipError_t e = hipGetDevice(&p->device);
     if (e == hipSuccess) e = hipMalloc((void **)&p->err, 16);
+    p->slot_bytes = slot_bytes(p->d);
+    if (e == hipSuccess && p->slot_bytes) e = hipMalloc((void **)&p->slots, p->slot_bytes);
     // a blocking copy: the word is zero before any later launch on any stream
     const int32_t zero[4] = {0, 0, 0, 0};
     if (e == hipSuccess) e = hipMemcpy(p->err, zero, 16, hipMemcpyHostToDevice);
     if (e != hipSuccess) {
         if (p->err) (void)hipFree(p->err);
+        if (p->slots) (void)hipFree(p->slots);
         free(p);
         return GEMM_RS_ERR_HIP;
     }
@@ -380,6 +658,8 @@ int gemm_grouped_run(gemm_grouped_plan_t p, const void *A, const void *B, const 
     a.offsets = (const int32_t *)offsets;
     a.C = C;
     a.err = p->err;
+    a.parts = 1;
+    a.slots = p->slots;
     hipStream_t s = (hipStream_t)stream;
     const int64_t c_elems = d.out_dtype == GEMM_RS_F32 ? 4 : 8;
     const bool wide = d.N % 8 == 0 && d.K % 8 == 0 && d.lda % 8 == 0 && d.ldb % 8 == 0 &&
@@ -405,7 +685,7 @@ int gemm_grouped_status(gemm_grouped_plan_t p, void *stream, int32_t *detail) {
 
 int gemm_grouped_query(gemm_grouped_plan_t p, gemm_grouped_info_t *info) {
     if (!p || !info) return GEMM_RS_ERR_INVALID_ARG;
-    info->workspace_bytes = 16;
+    info->workspace_bytes = 16 + p->slot_bytes;
     return GEMM_RS_OK;
 }
 
@@ -417,6 +697,7 @@ int gemm_grouped_destroy(gemm_grouped_plan_t p) {
         switched = hipSetDevice(p->device) == hipSuccess;
     // teardown is best effort: a failure here leaves nothing to undo
     (void)hipFree(p->err);
+    if (p->slots) (void)hipFree(p->slots);
     if (switched) (void)hipSetDevice(cur);
     free(p);
     return GEMM_RS_OK;

@@ -132,7 +132,8 @@ def test_rows_outside_groups_strides_and_alignment(op):
 
 @pytest.mark.parametrize("out", [F.BF16, F.F32])
 def test_accumulate(out):
-    for sizes, N, K in (([3, 0, 140], 136, 72), ([3, 0, 140], 33, 7), ([900, 0, 600], 512, 256)):
+    for sizes, N, K in (([3, 0, 140], 136, 72), ([3, 0, 140], 33, 7), ([900, 0, 600], 512, 256), ([2100, 1900], 264, 136),
+                        ([5000], 72, 200)):
         say("grouped accumulate", sizes, N, K)
         _run("TN", sizes, N, K, out=out, accumulate=1)
         _run("TN", sizes, N, K, out=out, accumulate=1, ternary=out == F.F32)
