@@ -490,8 +490,8 @@ double row_tiles(const GroupedArgs &a, int bm) {
 // Large tiles do the most work per byte, small ones fill the CUs; of equals the
 // larger, which reads B less often where an expert has more rows than the mean.
 // Measured, us for 256 x 256, 128 x 256, 128 x 128, 64 x 64 and 32 x 64 streams
-// (rows : N : K : E): 16384 : 3584 : 4096 : 8 453, 524, 633, -, -;
-// 8000 : 1792 : 4096 : 64 256, 221, 253, -, -; 512 : 3584 : 4096 : 8 104, 64, 50,
+// (rows : N : K : E): 16384 : 3584 : 4096 : 8 440, 490, 587, -, -;
+// 8000 : 1792 : 4096 : 64 254, 225, 247, -, -; 512 : 3584 : 4096 : 8 104, 64, 50,
 // 79, 92; 128 : 1024 : 2048 : 1 -, -, 20, 11, 8.4; 32 : 3584 : 4096 : 1 -, -, 35,
 // 18, 16.
 template <int OP>
@@ -500,7 +500,7 @@ hipError_t launch_rows(GroupedArgs &a, hipStream_t s) {
         int bm, bn;
         double step;
     };
-    const Option options[] = {{256, 256, 1.77}, {128, 256, 1.02}, {128, 128, 0.66}, {64, 64, 0.34}, {32, 64, 0.25}};
+    const Option options[] = {{256, 256, 1.7}, {128, 256, 0.96}, {128, 128, 0.6}, {64, 64, 0.34}, {32, 64, 0.25}};
     const double live = a.E < a.rows ? a.E : a.rows, steps = ceil_div((double)a.K, 64);
     const double floor_us = 2.0 * (live * a.K * a.N + (double)a.rows * (a.K + a.N)) / 5.0e6;
     int best = 0;

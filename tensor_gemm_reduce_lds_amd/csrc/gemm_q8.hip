@@ -280,9 +280,9 @@ hipError_t launch_product(const Q8Args &q, hipStream_t s) {
     // time, in us measured at K = 3584 (a round costs about as much where it
     // is not full).  Large tiles read fewer bytes per operation, small ones
     // fill the CUs when there are few.  Measured, us for 256 x 256, 128 x 128,
-    // 64 x 128, 64 x 64: 8192 x 8192 x 3584 236, 302, 361, 393; 1024 x 3584 x
-    // 8192 79, 47, 53, 62; 512 x 3584 x 8192 79, 39, 31, 36; 256 x 3584 x 8192
-    // 79, 38, 29, 25.
+    // 64 x 128, 64 x 64: 8192 x 8192 x 3584 236, 306, 359, 422; 1024 x 3584 x
+    // 8192 78, 39, 44, 57; 512 x 3584 x 8192 78, 31, 26, 28; 256 x 3584 x 8192
+    // 76, 30, 24, 19.
     auto rounds = [&](int64_t bm, int64_t bn) {
         return (double)((((q.M + bm - 1) / bm) * ((q.N + bn - 1) / bn) + kCus - 1) / kCus);
     };
@@ -290,10 +290,10 @@ hipError_t launch_product(const Q8Args &q, hipStream_t s) {
     const double t64w = 13 * rounds(64, 128), t64 = 2 + 8 * rounds(64, 64);
     if (t256 <= t128 && t256 <= t64w && t256 <= t64) return launch_tile<256, 256, 2, 4, 2>(q, s);
     // one round: deep loads, one workgroup per CU; more: two per CU (1000 x
-    // 4096 x 1792, 256 tiles: 15.0 / 16.2 us; 1000 x 4099, 264 tiles: 33.8 / 21.7)
+    // 4096 x 1792, 256 tiles: 14.0 / 15.7 us; 1000 x 4099, 264 tiles: 30.8 / 21.1)
     if (t128 <= t64w && t128 <= t64)
         return rounds(128, 128) <= 1 ? launch_tile<128, 128, 2, 4, 4>(q, s) : launch_tile<128, 128, 2, 4, 2>(q, s);
-    if (t64w <= t64) return launch_tile<64, 128, 2, 4, 3>(q, s);
+    if (t64w <= t64) return launch_tile<64, 128, 2, 2, 3>(q, s);
     return launch_tile<64, 64, 2, 2, 4>(q, s);
 }
 
@@ -386,6 +386,7 @@ int gemm_q8_quantize(const void *x, int32_t dtype, int64_t rows, int64_t cols, i
     auto of_type = [&](auto f32) {
         constexpr bool F = decltype(f32)::value;
         if (!vec) go(quantize_kernel<F, 1, 0, 256>, 256);
+        else if (cols <= 2048 && rows >= kCus) go(quantize_kernel<F, 8, 32, 64>, 64);
         else if (cols <= 2048) go(quantize_kernel<F, 8, 8, 256>, 256);
         else if (cols <= 8192) go(quantize_kernel<F, 8, 16, 512>, 512);
         else if (cols <= 16384) go(quantize_kernel<F, 8, 16, 1024>, 1024);

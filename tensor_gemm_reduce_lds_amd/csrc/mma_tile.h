@@ -110,6 +110,15 @@ struct Operand {
     const char *base;
     int64_t ld;
     int32_t span;
+
+    // The same in scalar registers (the values are the same in every lane).
+    __device__ __forceinline__ Operand scalar() const {
+        const uint64_t p = (uint64_t)base;
+        const uint32_t lo = __builtin_amdgcn_readfirstlane((int32_t)(uint32_t)p);
+        const uint32_t hi = __builtin_amdgcn_readfirstlane((int32_t)(uint32_t)(p >> 32));
+        return {(const char *)(((uint64_t)hi << 32) | lo),
+                (int64_t)__builtin_amdgcn_readfirstlane((int32_t)ld), __builtin_amdgcn_readfirstlane(span)};
+    }
 };
 
 template <class ACC, int BM_, int BN_, int WGM_, int WGN_, bool A_COL, bool B_COL, int STAGES>
@@ -119,17 +128,18 @@ struct Tile {
     static constexpr int WM = BM / WGM, WN = BN / WGN;
     static constexpr int FM = WM / 32, FN = WN / 32;
     static constexpr int KS = 4;                        // 32-byte slices of a step
+    // Slices whose fragments are read together: at least 4 matrix operations
+    // (of 32 cycles) to a batch, to cover the LDS latency of the next one.
+    static constexpr int SL = FM * FN >= 4 ? 1 : FM * FN >= 2 ? 2 : 4;
+    static constexpr int BATCHES = KS / SL;
     static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
     static constexpr int STAGE = A_BYTES + B_BYTES;
     static constexpr int LDS_BYTES = STAGES * STAGE;
-    // Loads of 1 KB per stage and operand, issued by DW waves.  With 8 waves
-    // only one wave of each SIMD (wave w runs on SIMD w % 4) loads, so the
-    // other one only feeds the matrix pipe.
-    static constexpr int DW = NW >= 8 ? NW / 2 : NW;
+    // Loads of 1 KB per stage and operand, dealt out to all waves.
+    static constexpr int DW = NW;
     static constexpr int AI = A_BYTES / 1024 / DW, BI = B_BYTES / 1024 / DW;
     static_assert(AI * DW * 1024 == A_BYTES && BI * DW * 1024 == B_BYTES, "whole loads per wave");
     static_assert(WM % 32 == 0 && WN % 32 == 0, "whole blocks per wave");
-    static_assert(DW * 8 == 32, "the row swizzle alternates with the load");
     static_assert(!A_COL || BM >= 128, "column swizzle needs 16 chunks per row");
     static_assert(!B_COL || BN >= 128, "column swizzle needs 16 chunks per row");
     static_assert(LDS_BYTES <= 160 * 1024, "LDS");
@@ -142,46 +152,29 @@ struct Tile {
 
     ACC acc[FM][FN];
 
-    // Load i of an operand covers the rows from i * ROWS of its window: the
-    // descriptor moves by ROWS rows and keeps the window's end, so rows past it
-    // read as zero, and a lane's offset takes at most two values (the row
-    // swizzle alternates with i).
-    template <bool COL, int B> static constexpr int load_rows() {
-        return COL ? DW * 64 / (B / 8) : DW * 8;
+    // Load i of wave w covers 1 KB of an operand's tile, at (i * DW + w) * 1024:
+    // this lane's chunk of it, and its offset from the window's base.
+    template <bool COL, int B>
+    static __device__ __forceinline__ int load_row(int i, int w, int lane) {
+        return COL ? (i * DW + w) * (64 / (B / 8)) + lane / (B / 8) : (i * DW + w) * 8 + lane / 8;
     }
     template <bool COL, int B>
-    static __device__ __forceinline__ int load_chunk(int odd, int dwave, int lane) {
-        if constexpr (COL) return (lane % (B / 8)) ^ col_swz(dwave * (64 / (B / 8)) + lane / (B / 8));
-        else return (lane & 7) ^ row_swz(odd * 32 + dwave * 8 + lane / 8);
+    static __device__ __forceinline__ int load_chunk(int i, int w, int lane) {
+        const int r = load_row<COL, B>(i, w, lane);
+        return COL ? (lane % (B / 8)) ^ col_swz(r) : (lane & 7) ^ row_swz(r);
     }
     template <bool COL, int B>
-    static __device__ __forceinline__ uint32_t load_offset(const Operand &o, int odd, int dwave, int lane) {
-        const int row = COL ? dwave * (64 / (B / 8)) + lane / (B / 8) : dwave * 8 + lane / 8;
-        return (uint32_t)row * (uint32_t)o.ld + (uint32_t)load_chunk<COL, B>(odd, dwave, lane) * 16u;
+    static __device__ __forceinline__ uint32_t load_offset(const Operand &o, int i, int w, int lane) {
+        return (uint32_t)load_row<COL, B>(i, w, lane) * (uint32_t)o.ld + (uint32_t)load_chunk<COL, B>(i, w, lane) * 16u;
     }
-    // Bytes of step kt's window, of which `left` (at most KE) elements, or
-    // rows of a column operand, are valid; and its base.
+    // Descriptor of step kt's window, of which `left` (at most KE, none if
+    // negative) elements, or rows of a column operand, are valid.  Rows past
+    // the operand's lie past its end.
     template <bool COL, int ELEM>
-    static __device__ __forceinline__ uint32_t window_bytes(const Operand &o, int left) {
-        if constexpr (COL) return (uint32_t)(left - 1) * (uint32_t)o.ld + (uint32_t)o.span;
-        else return (uint32_t)(o.span - 1) * (uint32_t)o.ld + (uint32_t)(left * ELEM);
-    }
-    template <bool COL>
-    static __device__ __forceinline__ const char *window_base(const Operand &o, int kt) {
-        return o.base + (COL ? (int64_t)kt * 64 * o.ld : (int64_t)kt * 128);
-    }
-    template <int I, bool COL, int B>
-    static __device__ __forceinline__ void load_part(const Operand &o, const char *base, uint32_t bytes,
-                                                     uint32_t voff, uint32_t lds, int dwave) {
-        const uint32_t skip = (uint32_t)I * load_rows<COL, B>() * (uint32_t)o.ld;
-        load_to_lds(buffer_of(base + skip, bytes > skip ? bytes - skip : 0u), voff,
-                    lds + (I * DW + dwave) * 1024);
-    }
-    template <bool COL, int B, int... I>
-    static __device__ __forceinline__ void load_all(std::integer_sequence<int, I...>, const Operand &o,
-                                                    const char *base, uint32_t bytes,
-                                                    const uint32_t (&voff)[2], uint32_t lds, int dwave) {
-        (load_part<I, COL, B>(o, base, bytes, voff[COL ? 0 : I & 1], lds, dwave), ...);
+    static __device__ __forceinline__ i32x4_t window(const Operand &o, int kt, int left) {
+        const uint32_t bytes = COL ? (uint32_t)(left - 1) * (uint32_t)o.ld + (uint32_t)o.span
+                                   : (uint32_t)(o.span - 1) * (uint32_t)o.ld + (uint32_t)(left * ELEM);
+        return buffer_of(o.base + (COL ? (int64_t)kt * 64 * o.ld : (int64_t)kt * 128), left > 0 ? bytes : 0u);
     }
 
     // Steps of a contraction of k elements, ELEM bytes each.
@@ -192,41 +185,48 @@ struct Tile {
     // acc = A . B over a contraction of `k` elements (of a column operand:
     // rows; ELEM bytes each in a row operand).
     template <int ELEM>
-    __device__ __forceinline__ void run(lds_t *smem, const Operand &a, const Operand &b, int32_t k) {
+    __device__ __forceinline__ void run(lds_t *smem, const Operand &a_in, const Operand &b_in, int32_t k_in) {
         constexpr int KE = 128 / ELEM;
         static_assert(!(A_COL || B_COL) || KE == 64, "column operands are bfloat16");
+        const Operand a = a_in.scalar(), b = b_in.scalar();
+        const int k = __builtin_amdgcn_readfirstlane(k_in);
         const int tid = threadIdx.x, lane = tid & 63;
         const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int wm = wave / WGN, wn = wave % WGN;
         const uint32_t smem_base = (uint32_t)(size_t)smem;
         const int KT = steps_of<ELEM>(k);
-        const int dwave = wave < DW ? wave : 0;
 
-        const uint32_t a_voff[2] = {load_offset<A_COL, BM>(a, 0, dwave, lane),
-                                    A_COL ? 0u : load_offset<A_COL, BM>(a, 1, dwave, lane)};
-        const uint32_t b_voff[2] = {load_offset<B_COL, BN>(b, 0, dwave, lane),
-                                    B_COL ? 0u : load_offset<B_COL, BN>(b, 1, dwave, lane)};
-
-        auto issue = [&](int kt, int st) __attribute__((always_inline)) {
-            if (wave >= DW) return;                     // wave-uniform
-            const int left = k - kt * KE < KE ? k - kt * KE : KE;
-            uint32_t av[2] = {a_voff[0], a_voff[1]}, bv[2] = {b_voff[0], b_voff[1]};
-            if (left < KE) {
-                // the last step of a contraction that is no multiple of KE:
-                // row chunks past its end are sent past the descriptor (a
-                // column operand's rows past it lie there already)
-                const int chunks = left * ELEM / 16;
+        uint32_t voff[AI + BI];
 #pragma unroll
-                for (int odd = 0; odd < 2; ++odd) {
-                    if (!A_COL && load_chunk<A_COL, BM>(odd, dwave, lane) >= chunks) av[odd] = 0xfffffff0u;
-                    if (!B_COL && load_chunk<B_COL, BN>(odd, dwave, lane) >= chunks) bv[odd] = 0xfffffff0u;
-                }
-            }
-            load_all<A_COL, BM>(std::make_integer_sequence<int, AI>{}, a, window_base<A_COL>(a, kt),
-                                window_bytes<A_COL, ELEM>(a, left), av, smem_base + st * A_BYTES, dwave);
-            load_all<B_COL, BN>(std::make_integer_sequence<int, BI>{}, b, window_base<B_COL>(b, kt),
-                                window_bytes<B_COL, ELEM>(b, left), bv,
-                                smem_base + STAGES * A_BYTES + st * B_BYTES, dwave);
+        for (int i = 0; i < AI; ++i) voff[i] = load_offset<A_COL, BM>(a, i, wave, lane);
+#pragma unroll
+        for (int i = 0; i < BI; ++i) voff[AI + i] = load_offset<B_COL, BN>(b, i, wave, lane);
+        // row swizzles repeat every 64 rows, so a row operand's loads have at
+        // most two chunk numbers; a column operand needs none (below)
+        const int a_chunk[2] = {load_chunk<A_COL, BM>(0, wave, lane), load_chunk<A_COL, BM>(1, wave, lane)};
+        const int b_chunk[2] = {load_chunk<B_COL, BN>(0, wave, lane), load_chunk<B_COL, BN>(1, wave, lane)};
+
+        // A step's loads, one at a time.  Past the contraction's last step
+        // they read nothing (and still count, so the waits are constants); in
+        // its last step, chunks past the end of row operands are sent past
+        // the descriptor (rows of column operands lie there already).
+        struct Load {
+            i32x4_t a, b;
+            int chunks, to;
+        };
+        auto begin_load = [&](int kt, int st) __attribute__((always_inline)) {
+            int left = k - kt * KE;
+            left = left < KE ? left : KE;
+            return Load{window<A_COL, ELEM>(a, kt, left), window<B_COL, ELEM>(b, kt, left), left * ELEM / 16, st};
+        };
+        auto load = [&](const Load &l, int i) __attribute__((always_inline)) {
+            const bool isa = i < AI;
+            const int j = isa ? i : i - AI;
+            uint32_t v = voff[i];
+            if (isa ? !A_COL : !B_COL)
+                v = (isa ? a_chunk : b_chunk)[DW == 8 ? 0 : j & 1] < l.chunks ? v : 0xfffffff0u;
+            load_to_lds(isa ? l.a : l.b, v,
+                        smem_base + (isa ? l.to * A_BYTES : STAGES * A_BYTES + l.to * B_BYTES) + (j * DW + wave) * 1024);
         };
 
         // LDS addresses of this lane's fragments: few registers, and constants
@@ -277,86 +277,99 @@ struct Tile {
             return __builtin_bit_cast(i32x4_t, both);
         };
         typedef __attribute__((address_space(3))) i32x4_t lds_i32x4;
-        auto load_frags = [&](int st, int ks, i32x4_t (&af)[FM], i32x4_t (&bf)[FN])
-            __attribute__((always_inline)) {
-#pragma unroll
-            for (int i = 0; i < FM; ++i) {
-                if constexpr (A_COL) af[i] = col_read(a_at[0][i] + st * A_BYTES + ks * 16 * BM * 2, BM);
-                else af[i] = *(lds_i32x4 *)(a_at[ks][i & 1] + st * A_BYTES + i * 4096);
-            }
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                if constexpr (B_COL) bf[j] = col_read(b_at[0][j] + st * B_BYTES + ks * 16 * BN * 2, BN);
-                else bf[j] = *(lds_i32x4 *)(b_at[ks][j & 1] + st * B_BYTES + j * 4096);
+        // Fragments are double-buffered in registers, SL slices of a step to a
+        // batch: while the matrix pipe works on one batch the next one is read.
+        constexpr int PER = FM + FN, READS = SL * PER, MM = SL * FM * FN, LOADS = AI + BI;
+        i32x4_t af[2][SL][FM], bf[2][SL][FN];
+        auto read = [&](int st, int batch, int fb, int r) __attribute__((always_inline)) {
+            const int s = r / PER, ks = batch * SL + s, i = r % PER, j = i - FM;
+            if (i < FM) {
+                if constexpr (A_COL) af[fb][s][i] = col_read(a_at[0][i] + st * A_BYTES + ks * 16 * BM * 2, BM);
+                else af[fb][s][i] = *(lds_i32x4 *)(a_at[ks][i & 1] + st * A_BYTES + i * 4096);
+            } else {
+                if constexpr (B_COL) bf[fb][s][j] = col_read(b_at[0][j] + st * B_BYTES + ks * 16 * BN * 2, BN);
+                else bf[fb][s][j] = *(lds_i32x4 *)(b_at[ks][j & 1] + st * B_BYTES + j * 4096);
             }
         };
-        // Fragments are double-buffered in registers: the next slice's LDS
-        // reads are spread between the current slice's matrix operations, and
-        // a step's last slice is issued behind the next step's barrier, where
-        // it covers the latency of that step's first reads.
-        i32x4_t af[2][FM], bf[2][FN];
+        auto mma_one = [&](int fb, int m) __attribute__((always_inline)) {
+            const int s = m / (FM * FN), i = m / FN % FM, j = m % FN;
+            acc[i][j] = mma(af[fb][s][i], bf[fb][s][j], acc[i][j]);
+        };
         auto mmas = [&](int fb) __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < FM; ++i)
-#pragma unroll
-                for (int j = 0; j < FN; ++j) acc[i][j] = mma(af[fb][i], bf[fb][j], acc[i][j]);
-        };
-        auto spread = [&]() __attribute__((always_inline)) {
-            constexpr int R = A_READS + B_READS, M = FM * FN;
-#pragma unroll
-            for (int m = 0; m < M; ++m) {
-                const int n = (m + 1) * R / M - m * R / M;
-                if (n == 1) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                if (n == 2) __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-                if (n == 3) __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
-                if (n >= 4) __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            }
+            for (int m = 0; m < MM; ++m) mma_one(fb, m);
         };
 #pragma unroll
-        for (int s = 0; s < STAGES - 1; ++s)
-            if (s < KT) issue(s, s);
-        auto step = [&](int kt, auto stage) __attribute__((always_inline)) {
+        for (int s = 0; s < STAGES - 1; ++s) {
+            const Load l = begin_load(s, s);
+#pragma unroll
+            for (int i = 0; i < LOADS; ++i) load(l, i);
+        }
+        // `parity`: of kt, a constant; `stage`: kt % STAGES; `zeroth`: kt is 0
+        auto step = [&](int kt, auto stage, auto parity, auto zeroth) __attribute__((always_inline)) {
             const int st = stage;
+            constexpr int P = decltype(parity)::value;
+            constexpr int first = BATCHES == 1 ? P : 0;    // buffer of the step's first batch
             // this wave's loads of step kt have landed (later steps' may be in
             // flight); behind the barrier every wave's have, and every wave
-            // has read the stage that the next issue overwrites
-            const int ahead = KT - 1 - kt;
-            wait_groups<AI + BI, STAGES - 2>(ahead);
+            // has read the stage that the next loads overwrite
+            wait_loads<(STAGES - 2) * LOADS>();
             lds_only_barrier();
-            load_frags(st, 0, af[0], bf[0]);
-            if (kt > 0) mmas(1);
-            if (kt + STAGES - 1 < KT) {
-                int to = st + STAGES - 1;
-                if (to >= STAGES) to -= STAGES;
-                issue(kt + STAGES - 1, to);
-            }
-            __builtin_amdgcn_sched_barrier(0);
+            int to = st + STAGES - 1;
+            if (to >= STAGES) to -= STAGES;
+            const Load l = begin_load(kt + STAGES - 1, to);
+            // A wave issues in order, and a read or a load waits its turn at
+            // the LDS or the memory pipeline, so they go one by one behind
+            // the matrix operations, which run meanwhile.
+            if constexpr (decltype(zeroth)::value) {
 #pragma unroll
-            for (int ks = 0; ks + 1 < KS; ++ks) {
-                load_frags(st, ks + 1, af[(ks + 1) & 1], bf[(ks + 1) & 1]);
-                mmas(ks & 1);
-                spread();
+                for (int r = 0; r < READS; ++r) read(st, 0, first, r);
+#pragma unroll
+                for (int i = 0; i < LOADS; ++i) load(l, i);
                 __builtin_amdgcn_sched_barrier(0);
             }
-        };
-        if constexpr (STAGES == 2) {
-            // two steps per turn: the stage is a constant, its offset goes
-            // into the LDS reads' immediate field
-            int kt = 0;
-            for (; kt + 1 < KT; kt += 2) {
-                step(kt, std::integral_constant<int, 0>{});
-                step(kt + 1, std::integral_constant<int, 1>{});
+#pragma unroll
+            for (int batch = decltype(zeroth)::value ? 1 : 0; batch < BATCHES; ++batch) {
+                const int into = (first + batch) & 1;
+#pragma unroll
+                for (int m = 0; m < MM; ++m) {
+                    mma_one(1 - into, m);
+#pragma unroll
+                    for (int r = m * READS / MM; r < (m + 1) * READS / MM; ++r) read(st, batch, into, r);
+                    if (batch == 0)
+#pragma unroll
+                        for (int i = m * LOADS / MM; i < (m + 1) * LOADS / MM; ++i) load(l, i);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
-            if (kt < KT) step(kt, std::integral_constant<int, 0>{});
-        } else {
-            int st = 0;
-            for (int kt = 0; kt < KT; ++kt) {
-                step(kt, st);
+        };
+        using Even = std::integral_constant<int, 0>;
+        using Odd = std::integral_constant<int, 1>;
+        // two steps per turn, so that fragment buffers, and with two stages
+        // the stage (which goes into the LDS reads' immediate field), are
+        // constants
+        using No = std::false_type;
+        if (KT > 0) step(0, Even{}, Even{}, std::true_type{});
+        int kt = 1, st = 1 % STAGES;
+        for (; kt + 1 < KT; kt += 2) {
+            if constexpr (STAGES == 2) {
+                step(kt, Odd{}, Odd{}, No{});
+                step(kt + 1, Even{}, Even{}, No{});
+            } else {
+                step(kt, st, Odd{}, No{});
+                if (++st == STAGES) st = 0;
+                step(kt + 1, st, Even{}, No{});
                 if (++st == STAGES) st = 0;
             }
         }
-        if (KT > 0) mmas(1);
+        if (kt < KT) {
+            if constexpr (STAGES == 2) step(kt, Odd{}, Odd{}, No{});
+            else step(kt, st, Odd{}, No{});
+        }
+        if (KT > 0) {
+            if (BATCHES > 1 || KT % 2 == 0) mmas(1);
+            else mmas(0);
+        }
     }
 
     // Hands the tile out as f(row, column, v[RUN]) for runs of RUN columns (8,
@@ -376,6 +389,7 @@ struct Tile {
         const int wm = wave / WGN, wn = wave % WGN;
         typedef __attribute__((address_space(3))) i32x4_t lds_i32x4;
         typedef __attribute__((address_space(3))) int32_t lds_i32;
+        wait_loads<0>();                                  // the empty loads past the last step
         lds_only_barrier();                               // every wave is done with the stages
 #pragma unroll
         for (int i = 0; i < FM; ++i) {

@@ -15,7 +15,7 @@ import re
 from typing import Optional
 
 from .gemm_rs import (BF16, ERR_HIP, ERR_INVALID_ARG, ERR_PROTOCOL, ERR_UNSUPPORTED, F32, OK,
-                      GemmRsError, _ptr, _stream_handle, gemm_rs_strerror, load_library)
+                      GemmRsError, _stream_handle, gemm_rs_strerror, load_library)
 
 __all__ = ["BF16", "F32", "OK", "ERR_INVALID_ARG", "ERR_UNSUPPORTED", "ERR_HIP", "ERR_PROTOCOL",
            "GROUPED_NN", "GROUPED_NT", "GROUPED_TN", "GemmRsError", "gemm_rs_strerror",
@@ -125,6 +125,12 @@ def _check(rc: int, where: str) -> None:
         raise GemmRsError(rc, where)
 
 
+def _addresses(*tensors):
+    """Device addresses of tensors (or addresses, or None), as `_ptr` of each:
+    one pass, since a call on few tokens takes less time than its marshalling."""
+    return [t if t is None or t.__class__ is int else t.data_ptr() for t in tensors]
+
+
 class _Plan:
     """Owns one plan handle of the family `_name`."""
 
@@ -139,6 +145,7 @@ class _Plan:
         _check(getattr(self._lib, self._name + "_plan")(ctypes.byref(desc), ctypes.byref(h)),
                self._name + "_plan")
         self.handle = h.value
+        self._run = getattr(self._lib, self._name + "_run")
 
     @property
     def info(self):
@@ -178,20 +185,20 @@ class BlockNormPlan(_Plan):
             has_y=has_y, post=post, pre=pre, quant=quant, backward=backward,
             rows_per_gate=rows_per_gate, res_scale=res_scale, weight_offset=weight_offset,
             eps_post=eps_post, eps_pre=eps_pre, **strides))
+        self._rows = rows
 
     def run(self, x, y, w_post, gate, w_pre, x_out, u, u_scale=None, rows=None, stream=None):
-        _check(self._lib.block_norm_run(
-            self.handle, _ptr(x), _ptr(y), _ptr(w_post), _ptr(gate), _ptr(w_pre), _ptr(x_out),
-            _ptr(u), _ptr(u_scale), self.desc.rows if rows is None else rows,
-            _stream_handle(stream)), "block_norm_run")
+        rc = self._run(self.handle, *_addresses(x, y, w_post, gate, w_pre, x_out, u, u_scale),
+                       self._rows if rows is None else rows, _stream_handle(stream))
+        if rc != OK:
+            raise GemmRsError(rc, "block_norm_run")
 
     def backward(self, dx_out, du, x_out, y, w_post, gate, w_pre, dx, dy, dw_post, dgate, dw_pre,
                  rows=None, stream=None):
         _check(self._lib.block_norm_backward(
-            self.handle, _ptr(dx_out), _ptr(du), _ptr(x_out), _ptr(y), _ptr(w_post), _ptr(gate),
-            _ptr(w_pre), _ptr(dx), _ptr(dy), _ptr(dw_post), _ptr(dgate), _ptr(dw_pre),
-            self.desc.rows if rows is None else rows, _stream_handle(stream)),
-            "block_norm_backward")
+            self.handle, *_addresses(dx_out, du, x_out, y, w_post, gate, w_pre, dx, dy, dw_post,
+                                     dgate, dw_pre),
+            self._rows if rows is None else rows, _stream_handle(stream)), "block_norm_backward")
 
 
 class Q8Plan(_Plan):
@@ -202,19 +209,24 @@ class Q8Plan(_Plan):
     def __init__(self, M, N, K, lda=0, ldw=0, ldd=0, out_dtype=BF16, has_bias=0):
         super().__init__(gemm_q8_desc_t(M=M, N=N, K=K, lda=lda, ldw=ldw, ldd=ldd,
                                         out_dtype=out_dtype, has_bias=has_bias))
+        self._rows = M
 
     def run(self, a, a_scale, w, w_scale, bias, D, rows=None, stream=None):
-        _check(self._lib.gemm_q8_run(
-            self.handle, _ptr(a), _ptr(a_scale), _ptr(w), _ptr(w_scale), _ptr(bias), _ptr(D),
-            self.desc.M if rows is None else rows, _stream_handle(stream)), "gemm_q8_run")
+        rc = self._run(self.handle, *_addresses(a, a_scale, w, w_scale, bias, D),
+                       self._rows if rows is None else rows, _stream_handle(stream))
+        if rc != OK:
+            raise GemmRsError(rc, "gemm_q8_run")
 
 
 def q8_quantize(x, q, scale, rows, cols, dtype=BF16, ldx=0, ldq=0, stream=None) -> None:
     """Rows of x to int8 rows and one scale per row (strides 0: tight, the
     int8 rows up to a multiple of 16)."""
-    _check(_library().gemm_q8_quantize(
-        _ptr(x), dtype, rows, cols, ldx or cols, _ptr(q), ldq or (cols + 15) // 16 * 16,
-        _ptr(scale), _stream_handle(stream)), "gemm_q8_quantize")
+    x, q, scale = _addresses(x, q, scale)
+    rc = (_lib or _library()).gemm_q8_quantize(x, dtype, rows, cols, ldx or cols, q,
+                                               ldq or (cols + 15) // 16 * 16, scale,
+                                               _stream_handle(stream))
+    if rc != OK:
+        raise GemmRsError(rc, "gemm_q8_quantize")
 
 
 class GroupedPlan(_Plan):
@@ -225,11 +237,13 @@ class GroupedPlan(_Plan):
     def __init__(self, M, N, K, E, op, out_dtype=BF16, accumulate=0, lda=0, ldb=0, ldc=0):
         super().__init__(gemm_grouped_desc_t(M=M, N=N, K=K, E=E, op=op, out_dtype=out_dtype,
                                              accumulate=accumulate, lda=lda, ldb=ldb, ldc=ldc))
+        self._rows = M
 
     def run(self, A, B, offsets, C, rows=None, stream=None):
-        _check(self._lib.gemm_grouped_run(
-            self.handle, _ptr(A), _ptr(B), _ptr(offsets), _ptr(C),
-            self.desc.M if rows is None else rows, _stream_handle(stream)), "gemm_grouped_run")
+        rc = self._run(self.handle, *_addresses(A, B, offsets, C),
+                       self._rows if rows is None else rows, _stream_handle(stream))
+        if rc != OK:
+            raise GemmRsError(rc, "gemm_grouped_run")
 
     def status(self, stream=None):
         """Returns (status, [code, expert, offsets[e], offsets[e+1]])."""
