@@ -225,8 +225,8 @@ __device__ __forceinline__ void store8(const GroupedArgs &p, int64_t row, int64_
 }
 
 // Sizes, strides and addresses that are multiples of 8 elements.
-template <int OP, int BM, int BN, int WGM, int WGN, int STAGES>
-using GroupedTile = Tile<f32x16_t, BM, BN, WGM, WGN, OP == GEMM_GROUPED_TN, OP != GEMM_GROUPED_NT, STAGES>;
+template <int OP, int BM, int BN, int WGM, int WGN, int SA, int SB>
+using GroupedTile = Tile<f32x16_t, BM, BN, WGM, WGN, OP == GEMM_GROUPED_TN, OP != GEMM_GROUPED_NT, SA, SB>;
 
 // A from the tile's first row, and expert e's B from column n0 (NN, NT).
 __device__ __forceinline__ Operand row_operand(const GroupedArgs &p, const RowTile &t, int32_t rows) {
@@ -240,9 +240,9 @@ __device__ __forceinline__ Operand column_operand(const GroupedArgs &p, int e, i
         return {(const char *)(p.B + ((int64_t)e * p.N + n0) * p.ldb), p.ldb * 2, cols};
 }
 
-template <int OP, int BM, int BN, int WGM, int WGN, int STAGES>
+template <int OP, int BM, int BN, int WGM, int WGN, int SA, int SB>
 __global__ __launch_bounds__(64 * WGM * WGN) void grouped_tile_kernel(GroupedArgs p) {
-    using T = GroupedTile<OP, BM, BN, WGM, WGN, STAGES>;
+    using T = GroupedTile<OP, BM, BN, WGM, WGN, SA, SB>;
     extern __shared__ __attribute__((aligned(1024))) char smem_generic[];
     lds_t *smem = (lds_t *)smem_generic;
     if (blockIdx.x == 0 && threadIdx.x < 64) check_offsets(p);
@@ -444,15 +444,15 @@ hipError_t launch_stream(GroupedArgs &a, hipStream_t s) {
     return launch_lds<grouped_stream_kernel<OP, MB, BN, NW, S>>(blocks, T::THREADS, T::LDS_BYTES, s, a);
 }
 
-template <int OP, int BM, int BN, int WGM, int WGN, int STAGES>
+template <int OP, int BM, int BN, int WGM, int WGN, int SA, int SB>
 hipError_t launch_tile(GroupedArgs &a, hipStream_t s) {
-    using T = GroupedTile<OP, BM, BN, WGM, WGN, STAGES>;
+    using T = GroupedTile<OP, BM, BN, WGM, WGN, SA, SB>;
     a.tiles_n = (int32_t)((a.N + BN - 1) / BN);
     a.tiles_m = (int32_t)((a.K + BM - 1) / BM);
     int64_t blocks;
     if (OP == GEMM_GROUPED_TN) blocks = (((int64_t)a.tiles_m * a.tiles_n * a.parts + 7) / 8) * 8 * a.E;
     else blocks = (a.rows / BM + (a.E < a.rows ? a.E : a.rows)) * a.tiles_n;
-    return launch_lds<grouped_tile_kernel<OP, BM, BN, WGM, WGN, STAGES>>(blocks, T::THREADS, T::LDS_BYTES, s, a);
+    return launch_lds<grouped_tile_kernel<OP, BM, BN, WGM, WGN, SA, SB>>(blocks, T::THREADS, T::LDS_BYTES, s, a);
 }
 
 // Adds the parts of every weight gradient, in their order.
@@ -515,9 +515,11 @@ hipError_t launch_rows(GroupedArgs &a, hipStream_t s) {
         }
     }
     switch (best) {
-    case 0: return launch_tile<OP, 256, 256, 2, 4, 2>(a, s);
-    case 1: return launch_tile<OP, 128, 256, 2, 4, 3>(a, s);
-    case 2: return launch_tile<OP, 128, 128, 2, 4, 4>(a, s);
+    case 0: return launch_tile<OP, 256, 256, 2, 4, 2, 3>(a, s);
+    case 1: return launch_tile<OP, 128, 256, 2, 4, 3, 3>(a, s);
+    case 2:    // one round: deep loads, one workgroup per CU; more: two per CU
+        if (row_tiles(a, 128) * ceil_div((double)a.N, 128) > kCus) return launch_tile<OP, 128, 128, 2, 4, 2, 3>(a, s);
+        return launch_tile<OP, 128, 128, 2, 4, 4, 4>(a, s);
     case 3: return launch_stream<OP, 2, 64, 4, 2>(a, s);
     default: return launch_stream<OP, 1, 64, 4, 3>(a, s);
     }
@@ -525,7 +527,7 @@ hipError_t launch_rows(GroupedArgs &a, hipStream_t s) {
 
 // TN: 256 x 256 tiles, or 128 x 128 with two workgroups per CU, so that one
 // stores while the other loads: better for short groups, whose time is the
-// stores (us for 256 / 128: 188 rows per expert 158 / 129, 2048 rows 440 / 564),
+// stores (us for 256 / 128: 188 rows per expert 158 / 126, 2048 rows 431 / 556),
 // and where there are fewer large tiles than CUs.  With few of the small ones
 // too, `parts` workgroups share a tile's rows and a second kernel adds them.
 struct TnChoice {
@@ -543,9 +545,9 @@ TnChoice tn_choice(int64_t rows, int64_t K, int64_t N, int64_t E) {
 }
 hipError_t launch_tn(GroupedArgs &a, hipStream_t s) {
     const TnChoice c = tn_choice(a.rows, a.K, a.N, a.E);
-    if (c.large) return launch_tile<GEMM_GROUPED_TN, 256, 256, 2, 4, 2>(a, s);
+    if (c.large) return launch_tile<GEMM_GROUPED_TN, 256, 256, 2, 4, 2, 2>(a, s);
     a.parts = c.parts;
-    hipError_t e = launch_tile<GEMM_GROUPED_TN, 128, 128, 2, 2, 2>(a, s);
+    hipError_t e = launch_tile<GEMM_GROUPED_TN, 128, 128, 2, 2, 2, 3>(a, s);
     if (e != hipSuccess || c.parts == 1) return e;
     const int64_t blocks = ((int64_t)a.E * a.K * (a.N / 8) + 255) / 256;
     hipLaunchKernelGGL(grouped_join_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s, a);

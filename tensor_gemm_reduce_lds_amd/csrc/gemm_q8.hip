@@ -33,9 +33,9 @@ __device__ __forceinline__ void store_one(const Q8Args &p, int64_t m, int64_t n,
 
 // BM x BN outputs per workgroup.  An XCD gets a run of the tiles in groups of 8
 // tile-rows, a group column by column.
-template <int BM, int BN, int WGM, int WGN, int STAGES>
+template <int BM, int BN, int WGM, int WGN, int SA, int SB>
 __global__ __launch_bounds__(64 * WGM * WGN) void q8_tile_kernel(Q8Args p) {
-    using T = Tile<i32x16_t, BM, BN, WGM, WGN, false, false, STAGES>;
+    using T = Tile<i32x16_t, BM, BN, WGM, WGN, false, false, SA, SB>;
     extern __shared__ __attribute__((aligned(1024))) char smem_generic[];
     lds_t *smem = (lds_t *)smem_generic;
     const uint32_t tn = (uint32_t)((p.N + BN - 1) / BN), tm = (uint32_t)((p.M + BM - 1) / BM);
@@ -69,10 +69,13 @@ __global__ __launch_bounds__(64 * WGM * WGN) void q8_tile_kernel(Q8Args p) {
             else store_vec<false, 8>(row_of(p.D, m, p.ldd, 2), (uint32_t)(n0 + c), x);
         });
     } else {
+        const int c1 = (int)threadIdx.x % BN;
+        const int64_t n = n0 + (c1 < n_left ? c1 : 0);
+        const float sw = p.w_scale[n], bias = p.bias ? p.bias[n] : 0.0f;
         tile.template store<1>(smem, [&](int r, int c, const int (&v)[1]) {
             if (r >= m_left || c >= n_left) return;
-            const int64_t m = m0 + r, n = n0 + c;
-            store_one(p, m, n, scaled(v[0], p.a_scale[m], p.w_scale[n], p.bias ? p.bias + n : nullptr));
+            const int64_t m = m0 + r;
+            store_one(p, m, n, scaled(v[0], p.a_scale[m], sw, p.bias ? &bias : nullptr));
         });
     }
 }
@@ -248,10 +251,10 @@ __global__ __launch_bounds__(THREADS) void quantize_kernel(const void *x, int64_
     }
 }
 
-template <int BM, int BN, int WGM, int WGN, int STAGES>
+template <int BM, int BN, int WGM, int WGN, int SA, int SB>
 hipError_t launch_tile(const Q8Args &q, hipStream_t s) {
-    using T = Tile<i32x16_t, BM, BN, WGM, WGN, false, false, STAGES>;
-    return launch_lds<q8_tile_kernel<BM, BN, WGM, WGN, STAGES>>(
+    using T = Tile<i32x16_t, BM, BN, WGM, WGN, false, false, SA, SB>;
+    return launch_lds<q8_tile_kernel<BM, BN, WGM, WGN, SA, SB>>(
         ((q.M + BM - 1) / BM) * ((q.N + BN - 1) / BN), T::THREADS, T::LDS_BYTES, s, q);
 }
 
@@ -276,25 +279,27 @@ hipError_t launch_product(const Q8Args &q, hipStream_t s) {
     if (q.M <= 32) return launch_few<2, 8, 3, 8, 2>(q, s);
     if (q.M <= 64) return launch_few<4, 8, 2, 4, 3>(q, s);
     if (q.M <= 128) return launch_few<8, 4, 2, 4, 2>(q, s);
-    // The tile with the least time: rounds of 256 workgroups times a round's
-    // time, in us measured at K = 3584 (a round costs about as much where it
-    // is not full).  Large tiles read fewer bytes per operation, small ones
-    // fill the CUs when there are few.  Measured, us for 256 x 256, 128 x 128,
-    // 64 x 128, 64 x 64: 8192 x 8192 x 3584 236, 306, 359, 422; 1024 x 3584 x
-    // 8192 78, 39, 44, 57; 512 x 3584 x 8192 78, 31, 26, 28; 256 x 3584 x 8192
-    // 76, 30, 24, 19.
+    // The tile with the least time, from the rounds of 256 workgroups that it
+    // makes (a round costs about as much where it is not full) and times
+    // measured at K = 3584, in us.  Large tiles read fewer bytes per operation,
+    // small ones fill the CUs when there are few.  One round takes deep loads
+    // and one workgroup per CU, more rounds two or three per CU.  Measured, us
+    // for 256 x 256, 128 x 128 (deep / two per CU), 64 x 128 (deep / three), 64 x
+    // 64: 8192 x 8192 x 3584 236, 354 / 306, 359 / -, 422; 1024 x 3584 x 8192 78,
+    // 39 / 44, 44 / 46, 57; 512 x 3584 x 8192 78, 31 / 38, 27 / 39, 28; 256 x 3584
+    // x 8192 76, 30 / -, 24 / -, 19; 1000 x 4104 x 1792 -, 24 / 21, - / 18, 21.
     auto rounds = [&](int64_t bm, int64_t bn) {
         return (double)((((q.M + bm - 1) / bm) * ((q.N + bn - 1) / bn) + kCus - 1) / kCus);
     };
-    const double t256 = 59 * rounds(256, 256), t128 = 19 * rounds(128, 128);
-    const double t64w = 13 * rounds(64, 128), t64 = 2 + 8 * rounds(64, 64);
-    if (t256 <= t128 && t256 <= t64w && t256 <= t64) return launch_tile<256, 256, 2, 4, 2>(q, s);
-    // one round: deep loads, one workgroup per CU; more: two per CU (1000 x
-    // 4096 x 1792, 256 tiles: 14.0 / 15.7 us; 1000 x 4099, 264 tiles: 30.8 / 21.1)
+    const double r128 = rounds(128, 128), r64w = rounds(64, 128);
+    const double t256 = 59 * rounds(256, 256), t128 = r128 <= 1 ? 18 : 20 * r128;
+    const double t64w = r64w <= 1 ? 13 : 4 + 11 * r64w, t64 = 2 + 8 * rounds(64, 64);
+    if (t256 <= t128 && t256 <= t64w && t256 <= t64) return launch_tile<256, 256, 2, 4, 2, 2>(q, s);
     if (t128 <= t64w && t128 <= t64)
-        return rounds(128, 128) <= 1 ? launch_tile<128, 128, 2, 4, 4>(q, s) : launch_tile<128, 128, 2, 4, 2>(q, s);
-    if (t64w <= t64) return launch_tile<64, 128, 2, 2, 3>(q, s);
-    return launch_tile<64, 64, 2, 2, 4>(q, s);
+        return r128 <= 1 ? launch_tile<128, 128, 2, 4, 4, 4>(q, s) : launch_tile<128, 128, 2, 4, 2, 3>(q, s);
+    if (t64w <= t64)
+        return r64w <= 1 ? launch_tile<64, 128, 2, 2, 3, 3>(q, s) : launch_tile<64, 128, 2, 2, 2, 2>(q, s);
+    return launch_tile<64, 64, 2, 2, 4, 4>(q, s);
 }
 
 int validate(const gemm_q8_desc_t &d) {

@@ -4,8 +4,9 @@
 // Each step takes 128 bytes of the contraction from a row operand (one row
 // of the contraction's 16-byte chunks per output row: 64 bfloat16, 128
 // int8), or the 64 rows of a column operand (bfloat16, stored with the
-// output axis contiguous).  Operands go from memory straight into a ring of
-// STAGES stages in LDS, 16 bytes per lane; loads run STAGES - 1 steps ahead.
+// output axis contiguous).  Operands go from memory straight into rings of
+// SA and SB stages in LDS, 16 bytes per lane; loads run SA - 1 and SB - 1 steps
+// ahead.
 // Both kinds of LDS tile are XOR-swizzled in 16-byte chunks (by choosing the
 // chunk that each lane fetches), so that fragment reads spread over the
 // banks; a column operand's fragments come from transposing LDS reads.
@@ -121,7 +122,7 @@ struct Operand {
     }
 };
 
-template <class ACC, int BM_, int BN_, int WGM_, int WGN_, bool A_COL, bool B_COL, int STAGES>
+template <class ACC, int BM_, int BN_, int WGM_, int WGN_, bool A_COL, bool B_COL, int SA, int SB = SA>
 struct Tile {
     static constexpr int BM = BM_, BN = BN_, WGM = WGM_, WGN = WGN_;
     static constexpr int NW = WGM * WGN, THREADS = 64 * NW;
@@ -133,8 +134,8 @@ struct Tile {
     static constexpr int SL = FM * FN >= 4 ? 1 : FM * FN >= 2 ? 2 : 4;
     static constexpr int BATCHES = KS / SL;
     static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
-    static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int LDS_BYTES = STAGES * STAGE;
+    static constexpr int LDS_BYTES = SA * A_BYTES + SB * B_BYTES;
+    static_assert(SA >= 2 && (SB == SA || SB == SA + 1), "rings of A and B stages");
     // Loads of 1 KB per stage and operand, dealt out to all waves.
     static constexpr int DW = NW;
     static constexpr int AI = A_BYTES / 1024 / DW, BI = B_BYTES / 1024 / DW;
@@ -196,6 +197,7 @@ struct Tile {
         const uint32_t smem_base = (uint32_t)(size_t)smem;
         const int KT = steps_of<ELEM>(k);
 
+        constexpr int B_AT = SA * A_BYTES;               // B's stages follow A's
         uint32_t voff[AI + BI];
 #pragma unroll
         for (int i = 0; i < AI; ++i) voff[i] = load_offset<A_COL, BM>(a, i, wave, lane);
@@ -212,21 +214,25 @@ struct Tile {
         // the descriptor (rows of column operands lie there already).
         struct Load {
             i32x4_t a, b;
-            int chunks, to;
+            int a_chunks, b_chunks, a_to, b_to;
         };
-        auto begin_load = [&](int kt, int st) __attribute__((always_inline)) {
-            int left = k - kt * KE;
-            left = left < KE ? left : KE;
-            return Load{window<A_COL, ELEM>(a, kt, left), window<B_COL, ELEM>(b, kt, left), left * ELEM / 16, st};
+        auto left_of = [&](int kt) __attribute__((always_inline)) {
+            const int left = k - kt * KE;
+            return left < KE ? left : KE;
+        };
+        auto begin_load = [&](int a_kt, int a_st, int b_kt, int b_st) __attribute__((always_inline)) {
+            const int al = left_of(a_kt), bl = left_of(b_kt);
+            return Load{window<A_COL, ELEM>(a, a_kt, al), window<B_COL, ELEM>(b, b_kt, bl),
+                        al * ELEM / 16, bl * ELEM / 16, a_st, b_st};
         };
         auto load = [&](const Load &l, int i) __attribute__((always_inline)) {
             const bool isa = i < AI;
             const int j = isa ? i : i - AI;
             uint32_t v = voff[i];
             if (isa ? !A_COL : !B_COL)
-                v = (isa ? a_chunk : b_chunk)[DW == 8 ? 0 : j & 1] < l.chunks ? v : 0xfffffff0u;
+                v = (isa ? a_chunk : b_chunk)[DW == 8 ? 0 : j & 1] < (isa ? l.a_chunks : l.b_chunks) ? v : 0xfffffff0u;
             load_to_lds(isa ? l.a : l.b, v,
-                        smem_base + (isa ? l.to * A_BYTES : STAGES * A_BYTES + l.to * B_BYTES) + (j * DW + wave) * 1024);
+                        smem_base + (isa ? l.a_to * A_BYTES : B_AT + l.b_to * B_BYTES) + (j * DW + wave) * 1024);
         };
 
         // LDS addresses of this lane's fragments: few registers, and constants
@@ -235,7 +241,6 @@ struct Tile {
         // i's parity.  Column operand: two transposing reads of 4 x 16 blocks,
         // of which this lane addresses row te, columns 4 tq..4 tq + 3; slices and
         // halves lie whole rows further, blocks differ in the swizzled chunk.
-        constexpr int B_AT = STAGES * A_BYTES;
         const int grp = lane >> 4, te = (lane & 15) >> 2, tq = lane & 3;
         lds_t *a_at[A_COL ? 1 : KS][A_COL ? FM : 2], *b_at[B_COL ? 1 : KS][B_COL ? FN : 2];
         auto col_at = [&](lds_t *tile, int x, int width) __attribute__((always_inline)) {
@@ -281,14 +286,14 @@ struct Tile {
         // batch: while the matrix pipe works on one batch the next one is read.
         constexpr int PER = FM + FN, READS = SL * PER, MM = SL * FM * FN, LOADS = AI + BI;
         i32x4_t af[2][SL][FM], bf[2][SL][FN];
-        auto read = [&](int st, int batch, int fb, int r) __attribute__((always_inline)) {
+        auto read = [&](int sa, int sb, int batch, int fb, int r) __attribute__((always_inline)) {
             const int s = r / PER, ks = batch * SL + s, i = r % PER, j = i - FM;
             if (i < FM) {
-                if constexpr (A_COL) af[fb][s][i] = col_read(a_at[0][i] + st * A_BYTES + ks * 16 * BM * 2, BM);
-                else af[fb][s][i] = *(lds_i32x4 *)(a_at[ks][i & 1] + st * A_BYTES + i * 4096);
+                if constexpr (A_COL) af[fb][s][i] = col_read(a_at[0][i] + sa * A_BYTES + ks * 16 * BM * 2, BM);
+                else af[fb][s][i] = *(lds_i32x4 *)(a_at[ks][i & 1] + sa * A_BYTES + i * 4096);
             } else {
-                if constexpr (B_COL) bf[fb][s][j] = col_read(b_at[0][j] + st * B_BYTES + ks * 16 * BN * 2, BN);
-                else bf[fb][s][j] = *(lds_i32x4 *)(b_at[ks][j & 1] + st * B_BYTES + j * 4096);
+                if constexpr (B_COL) bf[fb][s][j] = col_read(b_at[0][j] + sb * B_BYTES + ks * 16 * BN * 2, BN);
+                else bf[fb][s][j] = *(lds_i32x4 *)(b_at[ks][j & 1] + sb * B_BYTES + j * 4096);
             }
         };
         auto mma_one = [&](int fb, int m) __attribute__((always_inline)) {
@@ -299,31 +304,38 @@ struct Tile {
 #pragma unroll
             for (int m = 0; m < MM; ++m) mma_one(fb, m);
         };
+        // Step kt loads A's step kt + SA - 1 and B's step kt + SB - 1; the
+        // first steps' loads, in the same order.
 #pragma unroll
-        for (int s = 0; s < STAGES - 1; ++s) {
-            const Load l = begin_load(s, s);
+        for (int s = 1 - SB; s < 0; ++s) {
+            const Load l = begin_load(s + SA - 1, s + SA - 1, s + SB - 1, s + SB - 1);
 #pragma unroll
-            for (int i = 0; i < LOADS; ++i) load(l, i);
+            for (int i = s + SA - 1 < 0 ? AI : 0; i < LOADS; ++i) load(l, i);
         }
-        // `parity`: of kt, a constant; `stage`: kt % STAGES; `zeroth`: kt is 0
-        auto step = [&](int kt, auto stage, auto parity, auto zeroth) __attribute__((always_inline)) {
-            const int st = stage;
+        // Begins step kt: this wave's loads of it have landed (later steps' may
+        // be in flight); behind the barrier every wave's have, and every wave
+        // has read the stages that the loads of this step overwrite.
+        auto arrive = [&](int kt, int sa, int sb) __attribute__((always_inline)) {
+            wait_loads<(SA - 2) * LOADS + (SB > SA ? BI : 0)>();
+            lds_only_barrier();
+            int a_to = sa + SA - 1, b_to = sb + SB - 1;
+            if (a_to >= SA) a_to -= SA;
+            if (b_to >= SB) b_to -= SB;
+            return begin_load(kt + SA - 1, a_to, kt + SB - 1, b_to);
+        };
+        // `parity`: of kt, a constant; `sa`, `sb`: kt % SA, kt % SB; `zeroth`:
+        // kt is 0
+        auto step = [&](int kt, auto a_stage, auto b_stage, auto parity, auto zeroth) __attribute__((always_inline)) {
+            const int sa = a_stage, sb = b_stage;
             constexpr int P = decltype(parity)::value;
             constexpr int first = BATCHES == 1 ? P : 0;    // buffer of the step's first batch
-            // this wave's loads of step kt have landed (later steps' may be in
-            // flight); behind the barrier every wave's have, and every wave
-            // has read the stage that the next loads overwrite
-            wait_loads<(STAGES - 2) * LOADS>();
-            lds_only_barrier();
-            int to = st + STAGES - 1;
-            if (to >= STAGES) to -= STAGES;
-            const Load l = begin_load(kt + STAGES - 1, to);
+            const Load l = arrive(kt, sa, sb);
             // A wave issues in order, and a read or a load waits its turn at
             // the LDS or the memory pipeline, so they go one by one behind
             // the matrix operations, which run meanwhile.
             if constexpr (decltype(zeroth)::value) {
 #pragma unroll
-                for (int r = 0; r < READS; ++r) read(st, 0, first, r);
+                for (int r = 0; r < READS; ++r) read(sa, sb, 0, first, r);
 #pragma unroll
                 for (int i = 0; i < LOADS; ++i) load(l, i);
                 __builtin_amdgcn_sched_barrier(0);
@@ -335,7 +347,7 @@ struct Tile {
                 for (int m = 0; m < MM; ++m) {
                     mma_one(1 - into, m);
 #pragma unroll
-                    for (int r = m * READS / MM; r < (m + 1) * READS / MM; ++r) read(st, batch, into, r);
+                    for (int r = m * READS / MM; r < (m + 1) * READS / MM; ++r) read(sa, sb, batch, into, r);
                     if (batch == 0)
 #pragma unroll
                         for (int i = m * LOADS / MM; i < (m + 1) * LOADS / MM; ++i) load(l, i);
@@ -345,27 +357,38 @@ struct Tile {
         };
         using Even = std::integral_constant<int, 0>;
         using Odd = std::integral_constant<int, 1>;
-        // two steps per turn, so that fragment buffers, and with two stages
-        // the stage (which goes into the LDS reads' immediate field), are
-        // constants
+        // two steps per turn, so that fragment buffers, and stages of a ring
+        // of two (which go into the LDS reads' immediate field), are constants
         using No = std::false_type;
-        if (KT > 0) step(0, Even{}, Even{}, std::true_type{});
-        int kt = 1, st = 1 % STAGES;
-        for (; kt + 1 < KT; kt += 2) {
-            if constexpr (STAGES == 2) {
-                step(kt, Odd{}, Odd{}, No{});
-                step(kt + 1, Even{}, Even{}, No{});
-            } else {
-                step(kt, st, Odd{}, No{});
-                if (++st == STAGES) st = 0;
-                step(kt + 1, st, Even{}, No{});
-                if (++st == STAGES) st = 0;
+        int kt = 0, sa = 0, sb = 0;
+        auto next = [&]() __attribute__((always_inline)) {
+            ++kt;
+            if (++sa == SA) sa = 0;
+            if (++sb == SB) sb = 0;
+        };
+        // a wave whose rows or columns all lie past the output's only loads
+        const int rows = A_COL ? a.span / 2 : a.span, cols = B_COL ? b.span / 2 : b.span;
+        if (wm * WM >= rows || wn * WN >= cols) {
+            while (kt < KT) {
+                const Load l = arrive(kt, sa, sb);
+#pragma unroll
+                for (int i = 0; i < LOADS; ++i) load(l, i);
+                next();
             }
+            return;
         }
-        if (kt < KT) {
-            if constexpr (STAGES == 2) step(kt, Odd{}, Odd{}, No{});
-            else step(kt, st, Odd{}, No{});
+        auto turn = [&](auto parity, auto zeroth) __attribute__((always_inline)) {
+            if constexpr (SB == 2) step(kt, parity, parity, parity, zeroth);
+            else if constexpr (SA == 2) step(kt, parity, sb, parity, zeroth);
+            else step(kt, sa, sb, parity, zeroth);
+            next();
+        };
+        if (KT > 0) turn(Even{}, std::true_type{});
+        while (kt + 1 < KT) {
+            turn(Odd{}, No{});
+            turn(Even{}, No{});
         }
+        if (kt < KT) turn(Odd{}, No{});
         if (KT > 0) {
             if (BATCHES > 1 || KT % 2 == 0) mmas(1);
             else mmas(0);
@@ -423,8 +446,12 @@ struct Tile {
                     f((rr >> 5) * WM + i * 32 + (rr & 31), (tid % LPR) * 8, v);
                 }
             } else {
-                for (int u = tid; u < SROWS * BN; u += THREADS) {
-                    const int rr = u / BN, c = u % BN;
+                // a thread's columns are all tid % BN
+                static_assert(THREADS % BN == 0, "whole rows per turn");
+                const int c = tid % BN;
+#pragma unroll 8
+                for (int u = 0; u < SROWS; u += THREADS / BN) {
+                    const int rr = u + tid / BN;
                     const int v[1] = {*(lds_i32 *)(s + rr * ROW + (((c >> 2) ^ (rr & 15)) << 4) + (c & 3) * 4)};
                     f((rr >> 5) * WM + i * 32 + (rr & 31), c, v);
                 }
