@@ -39,27 +39,28 @@ struct NormArgs {
     float *part;
 };
 
-template <int VEC>
-__device__ __forceinline__ void load_param(const NormArgs &a, const void *p, uint32_t i, float add,
-                                           float *out) {
+// Columns c..c+7 of a row of parameters.
+template <bool WIDE>
+__device__ __forceinline__ void load_param(const NormArgs &a, const void *row, uint32_t c, float add, float *out) {
+    const uint32_t cols = (uint32_t)a.cols;
     if (a.param_f32) {
-        Raw<true, VEC> r;
-        load_raw(r, p, i);
+        Raw<true> r;
+        load8<true, WIDE>(r, row, c, cols);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) out[e] = raw_at(r, e) + add;
+        for (int e = 0; e < 8; ++e) out[e] = raw_at(r, e) + add;
     } else {
-        Raw<false, VEC> r;
-        load_raw(r, p, i);
+        Raw<false> r;
+        load8<false, WIDE>(r, row, c, cols);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) out[e] = raw_at(r, e) + add;
+        for (int e = 0; e < 8; ++e) out[e] = raw_at(r, e) + add;
     }
 }
 
 // THREADS threads hold a row of up to THREADS * EPT columns: thread t has
-// the VEC columns from (k * THREADS + t) * VEC for k < EPT / VEC.
-template <int VEC, int EPT, int THREADS, bool SF, bool YF, bool QUANT>
+// the 8 columns from (k * THREADS + t) * 8 for k < EPT / 8.
+template <bool WIDE, int EPT, int THREADS, bool SF, bool YF, bool QUANT>
 __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
-    constexpr int VPT = EPT / VEC;
+    constexpr int VPT = EPT / 8;
     __shared__ float slots[2 * 16];
     int turn = 0;
     const int tid = threadIdx.x;
@@ -69,44 +70,44 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
     float w_post[EPT], w_pre[EPT], gate[EPT];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
-        float *wo = w_post + k * VEC, *wp = w_pre + k * VEC, *g = gate + k * VEC;
+        const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
+        float *wo = w_post + k * 8, *wp = w_pre + k * 8, *g = gate + k * 8;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) wo[e] = wp[e] = g[e] = 1.0f;
+        for (int e = 0; e < 8; ++e) wo[e] = wp[e] = g[e] = 1.0f;
         if (c < cols) {
-            if (a.post) load_param<VEC>(a, a.w_post, c, a.weight_offset, wo);
-            if (a.pre) load_param<VEC>(a, a.w_pre, c, a.weight_offset, wp);
+            if (a.post) load_param<WIDE>(a, a.w_post, c, a.weight_offset, wo);
+            if (a.pre) load_param<WIDE>(a, a.w_pre, c, a.weight_offset, wp);
         }
     }
     int64_t gate_row = -1;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        Raw<SF, VEC> xr[VPT];
-        Raw<YF, VEC> yr[VPT];
+        Raw<SF> xr[VPT];
+        Raw<YF> yr[VPT];
         float x[EPT], y[EPT];
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
-            xr[k] = Raw<SF, VEC>{};
-            yr[k] = Raw<YF, VEC>{};
+            const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
+            xr[k] = Raw<SF>{};
+            yr[k] = Raw<YF>{};
             if (c < cols) {
-                load_raw(xr[k], row_of(a.x, row, a.ld_x, SF ? 4 : 2), c);
-                if (a.has_y) load_raw(yr[k], row_of(a.y, row, a.ld_y, YF ? 4 : 2), c);
+                load8<SF, WIDE>(xr[k], row_of(a.x, row, a.ld_x, SF ? 4 : 2), c, cols);
+                if (a.has_y) load8<YF, WIDE>(yr[k], row_of(a.y, row, a.ld_y, YF ? 4 : 2), c, cols);
             }
         }
         if (a.gated && row / a.rows_per_gate != gate_row) {
             gate_row = row / a.rows_per_gate;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
-                if (c < cols) load_param<VEC>(a, row_of(a.gate, gate_row, a.cols, a.param_f32 ? 4 : 2), c, 0.0f, gate + k * VEC);
+                const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
+                if (c < cols) load_param<WIDE>(a, row_of(a.gate, gate_row, a.cols, a.param_f32 ? 4 : 2), c, 0.0f, gate + k * 8);
             }
         }
 #pragma unroll
         for (int k = 0; k < VPT; ++k)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                x[k * VEC + e] = raw_at(xr[k], e);
-                y[k * VEC + e] = raw_at(yr[k], e);
+            for (int e = 0; e < 8; ++e) {
+                x[k * 8 + e] = raw_at(xr[k], e);
+                y[k * 8 + e] = raw_at(yr[k], e);
             }
         if (a.has_y) {
             float r2 = 1.0f;
@@ -119,13 +120,13 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
             }
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
+                const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) {
-                    const int i = k * VEC + e;
+                for (int e = 0; e < 8; ++e) {
+                    const int i = k * 8 + e;
                     x[i] = a.res_scale * x[i] + gate[i] * (y[i] * r2 * w_post[i]);
                 }
-                if (c < cols) store_vec<SF, VEC>(row_of(a.x_out, row, a.ld_x_out, SF ? 4 : 2), c, x + k * VEC);
+                if (c < cols) store8<SF, WIDE>(row_of(a.x_out, row, a.ld_x_out, SF ? 4 : 2), c, cols, x + k * 8);
             }
         }
         if (!a.pre) continue;
@@ -133,8 +134,8 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
 #pragma unroll
         for (int k = 0; k < VPT; ++k)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                s[0] += x[k * VEC + e] * x[k * VEC + e];   // columns past the row hold zeros
+            for (int e = 0; e < 8; ++e)
+                s[0] += x[k * 8 + e] * x[k * 8 + e];   // columns past the row hold zeros
         block_join<Sum, THREADS, 1>(s, slots, turn);
         const float r1 = 1.0f / sqrtf(s[0] * inv_cols + a.eps_pre);
 #pragma unroll
@@ -148,40 +149,32 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
             if (tid == 0) a.u_scale[row] = q.scale;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
+                const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
                 if (c >= cols) continue;
-                int8_t *to = (int8_t *)row_of(a.u, row, a.ld_u, 1) + c;
-                if constexpr (VEC == 8) {
-                    u32x2_t w = {0u, 0u};
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        w[e >> 2] |= (uint32_t)(quant_one(q, x[k * VEC + e]) & 0xff) << (8 * (e & 3));
-                    *(u32x2_t *)to = w;
-                } else {
-                    *to = (int8_t)quant_one(q, x[k]);
-                }
+                quant8<WIDE>(q, (int8_t *)row_of(a.u, row, a.ld_u, 1), c, cols,
+                             [&](int e) { return x[k * 8 + e]; });
             }
         } else {
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
-                const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
-                if (c < cols) store_vec<YF, VEC>(row_of(a.u, row, a.ld_u, YF ? 4 : 2), c, x + k * VEC);
+                const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
+                if (c < cols) store8<YF, WIDE>(row_of(a.u, row, a.ld_u, YF ? 4 : 2), c, cols, x + k * 8);
             }
         }
     }
 }
 
 // A row's inputs of the backward, as they lie in memory.
-template <int VEC, int VPT, bool SF, bool YF>
+template <int VPT, bool SF, bool YF>
 struct BackwardRow {
-    Raw<SF, VEC> x[VPT], d[VPT];
-    Raw<YF, VEC> y[VPT], u[VPT];
+    Raw<SF> x[VPT], d[VPT];
+    Raw<YF> y[VPT], u[VPT];
 };
 
-template <int VEC, int EPT, int THREADS, bool SF, bool YF, bool AHEAD>
+template <bool WIDE, int EPT, int THREADS, bool SF, bool YF, bool AHEAD>
 __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
-    constexpr int VPT = EPT / VEC;
-    using Row = BackwardRow<VEC, VPT, SF, YF>;
+    constexpr int VPT = EPT / 8;
+    using Row = BackwardRow<VPT, SF, YF>;
     __shared__ float slots[2 * 3 * 16];
     int turn = 0;
     const int tid = threadIdx.x;
@@ -197,32 +190,32 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
     float w_pre[EPT], gw[EPT], s_dy[EPT], s_post[EPT], s_pre[EPT];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
-        float *wo = gw + k * VEC, *wp = w_pre + k * VEC;
+        const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
+        float *wo = gw + k * 8, *wp = w_pre + k * 8;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const int i = k * VEC + e;
+        for (int e = 0; e < 8; ++e) {
+            const int i = k * 8 + e;
             wo[e] = wp[e] = 1.0f;
             s_dy[i] = s_post[i] = s_pre[i] = 0.0f;
         }
         if (c < cols) {
-            if (a.post) load_param<VEC>(a, a.w_post, c, a.weight_offset, wo);
-            if (a.pre) load_param<VEC>(a, a.w_pre, c, a.weight_offset, wp);
+            if (a.post) load_param<WIDE>(a, a.w_post, c, a.weight_offset, wo);
+            if (a.pre) load_param<WIDE>(a, a.w_pre, c, a.weight_offset, wp);
         }
     }
     auto take = [&](Row &r, int64_t row) __attribute__((always_inline)) {
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
-            r.x[k] = r.d[k] = Raw<SF, VEC>{};
-            r.y[k] = r.u[k] = Raw<YF, VEC>{};
+            const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
+            r.x[k] = r.d[k] = Raw<SF>{};
+            r.y[k] = r.u[k] = Raw<YF>{};
             if (c < cols && row < last) {
                 if (a.pre) {
-                    load_raw(r.x[k], row_of(a.x_out, row, a.ld_x_out, SF ? 4 : 2), c);
-                    load_raw(r.u[k], row_of(a.du, row, a.ld_du, YF ? 4 : 2), c);
+                    load8<SF, WIDE>(r.x[k], row_of(a.x_out, row, a.ld_x_out, SF ? 4 : 2), c, cols);
+                    load8<YF, WIDE>(r.u[k], row_of(a.du, row, a.ld_du, YF ? 4 : 2), c, cols);
                 }
-                if (a.has_y) load_raw(r.y[k], row_of(a.y, row, a.ld_y, YF ? 4 : 2), c);
-                if (a.dx_out) load_raw(r.d[k], row_of(a.dx_out, row, a.ld_dx_out, SF ? 4 : 2), c);
+                if (a.has_y) load8<YF, WIDE>(r.y[k], row_of(a.y, row, a.ld_y, YF ? 4 : 2), c, cols);
+                if (a.dx_out) load8<SF, WIDE>(r.d[k], row_of(a.dx_out, row, a.ld_dx_out, SF ? 4 : 2), c, cols);
             }
         }
     };
@@ -239,21 +232,21 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
                           : a.part + ((int64_t)blockIdx.x * 4 + (gate_row == first / a.rows_per_gate ? 2 : 3)) * a.cols;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
+            const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
             if (c >= cols) continue;
-            float g[VEC], w[VEC];
-            load_param<VEC>(a, row_of(a.gate, gate_row, a.cols, a.param_f32 ? 4 : 2), c, 0.0f, g);
+            float g[8], w[8];
+            load_param<WIDE>(a, row_of(a.gate, gate_row, a.cols, a.param_f32 ? 4 : 2), c, 0.0f, g);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) w[e] = 1.0f;
-            if (a.post) load_param<VEC>(a, a.w_post, c, a.weight_offset, w);
+            for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+            if (a.post) load_param<WIDE>(a, a.w_post, c, a.weight_offset, w);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                float &s = s_dy[k * VEC + e];
-                s_post[k * VEC + e] += g[e] * s;
+            for (int e = 0; e < 8; ++e) {
+                float &s = s_dy[k * 8 + e];
+                s_post[k * 8 + e] += g[e] * s;
                 w[e] *= s;
                 s = 0.0f;
             }
-            store_vec<true, VEC>(to, c, w);
+            store8<true, WIDE>(to, c, cols, w);
         }
     };
     auto begin_gate = [&](int64_t row) __attribute__((always_inline)) {
@@ -261,16 +254,16 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
         gate_end = (gate_row + 1) * a.rows_per_gate;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
+            const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
             if (c >= cols) continue;
-            float g[VEC];
-            float *w = gw + k * VEC;
-            load_param<VEC>(a, row_of(a.gate, gate_row, a.cols, a.param_f32 ? 4 : 2), c, 0.0f, g);
+            float g[8];
+            float *w = gw + k * 8;
+            load_param<WIDE>(a, row_of(a.gate, gate_row, a.cols, a.param_f32 ? 4 : 2), c, 0.0f, g);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) w[e] = 1.0f;
-            if (a.post) load_param<VEC>(a, a.w_post, c, a.weight_offset, w);
+            for (int e = 0; e < 8; ++e) w[e] = 1.0f;
+            if (a.post) load_param<WIDE>(a, a.w_post, c, a.weight_offset, w);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) w[e] *= g[e];
+            for (int e = 0; e < 8; ++e) w[e] *= g[e];
         }
     };
 
@@ -292,8 +285,8 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
 #pragma unroll
         for (int k = 0; k < VPT; ++k)
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const int i = k * VEC + e;
+            for (int e = 0; e < 8; ++e) {
+                const int i = k * 8 + e;
                 const float x = raw_at(r.x[k], e), y = raw_at(r.y[k], e);
                 s[0] += x * x;
                 s[1] += raw_at(r.u[k], e) * w_pre[i] * x;
@@ -307,11 +300,11 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
         float t[1] = {0.0f};
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
-            float dx[VEC];
+            const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
+            float dx[8];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-                const int i = k * VEC + e;
+            for (int e = 0; e < 8; ++e) {
+                const int i = k * 8 + e;
                 const float xh = raw_at(r.x[k], e) * r1, du = raw_at(r.u[k], e);
                 float d = raw_at(r.d[k], e);
                 if (a.pre) d += r1 * (du * w_pre[i] - xh * m1);
@@ -322,7 +315,7 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
                 b[i] = d * gw[i];
                 t[0] += b[i] * yh;
             }
-            if (c < cols) store_vec<SF, VEC>(row_of(a.dx, row, a.ld_dx, SF ? 4 : 2), c, dx);
+            if (c < cols) store8<SF, WIDE>(row_of(a.dx, row, a.ld_dx, SF ? 4 : 2), c, cols, dx);
         }
         if (!a.has_y) continue;
         float m2 = 0.0f;
@@ -332,12 +325,12 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
         }
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
-            float dy[VEC];
+            const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
+            float dy[8];
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                dy[e] = r2 * (b[k * VEC + e] - raw_at(r.y[k], e) * r2 * m2);
-            if (c < cols) store_vec<YF, VEC>(row_of(a.dy, row, a.ld_dy, YF ? 4 : 2), c, dy);
+            for (int e = 0; e < 8; ++e)
+                dy[e] = r2 * (b[k * 8 + e] - raw_at(r.y[k], e) * r2 * m2);
+            if (c < cols) store8<YF, WIDE>(row_of(a.dy, row, a.ld_dy, YF ? 4 : 2), c, cols, dy);
         }
     }
     if (a.gated) {
@@ -349,10 +342,10 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
     float *part = a.part + (int64_t)blockIdx.x * 4 * a.cols;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-        const uint32_t c = (uint32_t)(k * THREADS + tid) * VEC;
+        const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
         if (c >= cols) continue;
-        if (a.post) store_vec<true, VEC>(part, c, s_post + k * VEC);
-        if (a.pre) store_vec<true, VEC>(part + a.cols, c, s_pre + k * VEC);
+        if (a.post) store8<true, WIDE>(part, c, cols, s_post + k * 8);
+        if (a.pre) store8<true, WIDE>(part + a.cols, c, cols, s_pre + k * 8);
     }
 }
 
@@ -409,78 +402,66 @@ __global__ void norm_zero_kernel(float *a, float *b, int64_t n) {
     }
 }
 
-template <int VEC, int EPT, int THREADS>
+template <bool WIDE, int EPT, int THREADS>
 void launch_forward(const NormArgs &a, bool sf, bool yf, bool quant, int64_t grid, hipStream_t s) {
     auto go = [&](auto *kernel) {
         hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(THREADS), 0, s, a);
     };
     if (quant) {
-        if (sf && yf) go(norm_forward_kernel<VEC, EPT, THREADS, true, true, true>);
-        else if (sf) go(norm_forward_kernel<VEC, EPT, THREADS, true, false, true>);
-        else if (yf) go(norm_forward_kernel<VEC, EPT, THREADS, false, true, true>);
-        else go(norm_forward_kernel<VEC, EPT, THREADS, false, false, true>);
+        if (sf && yf) go(norm_forward_kernel<WIDE, EPT, THREADS, true, true, true>);
+        else if (sf) go(norm_forward_kernel<WIDE, EPT, THREADS, true, false, true>);
+        else if (yf) go(norm_forward_kernel<WIDE, EPT, THREADS, false, true, true>);
+        else go(norm_forward_kernel<WIDE, EPT, THREADS, false, false, true>);
     } else {
-        if (sf && yf) go(norm_forward_kernel<VEC, EPT, THREADS, true, true, false>);
-        else if (sf) go(norm_forward_kernel<VEC, EPT, THREADS, true, false, false>);
-        else if (yf) go(norm_forward_kernel<VEC, EPT, THREADS, false, true, false>);
-        else go(norm_forward_kernel<VEC, EPT, THREADS, false, false, false>);
+        if (sf && yf) go(norm_forward_kernel<WIDE, EPT, THREADS, true, true, false>);
+        else if (sf) go(norm_forward_kernel<WIDE, EPT, THREADS, true, false, false>);
+        else if (yf) go(norm_forward_kernel<WIDE, EPT, THREADS, false, true, false>);
+        else go(norm_forward_kernel<WIDE, EPT, THREADS, false, false, false>);
     }
 }
 
-template <int VEC, int EPT, int THREADS>
+template <bool WIDE, int EPT, int THREADS>
 void launch_backward(const NormArgs &a, bool sf, bool yf, int64_t grid, hipStream_t s) {
     auto go = [&](auto *kernel) {
         hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(THREADS), 0, s, a);
     };
-    constexpr bool AHEAD = VEC == 8 && (EPT == 8 || THREADS < 1024);
-    if (sf && yf) go(norm_backward_kernel<VEC, EPT, THREADS, true, true, AHEAD>);
-    else if (sf) go(norm_backward_kernel<VEC, EPT, THREADS, true, false, AHEAD>);
-    else if (yf) go(norm_backward_kernel<VEC, EPT, THREADS, false, true, AHEAD>);
-    else go(norm_backward_kernel<VEC, EPT, THREADS, false, false, AHEAD>);
+    constexpr bool AHEAD = EPT == 8 || THREADS < 1024;
+    if (sf && yf) go(norm_backward_kernel<WIDE, EPT, THREADS, true, true, AHEAD>);
+    else if (sf) go(norm_backward_kernel<WIDE, EPT, THREADS, true, false, AHEAD>);
+    else if (yf) go(norm_backward_kernel<WIDE, EPT, THREADS, false, true, AHEAD>);
+    else go(norm_backward_kernel<WIDE, EPT, THREADS, false, false, AHEAD>);
 }
 
 // Threads of a workgroup and columns of a row per thread.
-template <int VEC_, int EPT_, int THREADS_>
+template <int EPT_, int THREADS_>
 struct Shape {
-    static constexpr int VEC = VEC_, EPT = EPT_, THREADS = THREADS_;
+    static constexpr int EPT = EPT_, THREADS = THREADS_;
 };
 
 // Calls f with the kernel shape of a row length.
 template <class F>
-void forward_shape(int64_t cols, bool vec, F f) {
-    if (vec) {
-        if (cols <= 512) f(Shape<8, 8, 64>{});
-        else if (cols <= 2048) f(Shape<8, 8, 256>{});
-        else if (cols <= 4096) f(Shape<8, 8, 512>{});
-        else if (cols <= 8192) f(Shape<8, 8, 1024>{});
-        else f(Shape<8, 16, 1024>{});
-    } else {
-        if (cols <= 2048) f(Shape<1, 8, 256>{});
-        else if (cols <= 8192) f(Shape<1, 8, 1024>{});
-        else f(Shape<1, 16, 1024>{});
-    }
+void forward_shape(int64_t cols, F f) {
+    if (cols <= 512) f(Shape<8, 64>{});
+    else if (cols <= 2048) f(Shape<8, 256>{});
+    else if (cols <= 4096) f(Shape<8, 512>{});
+    else if (cols <= 8192) f(Shape<8, 1024>{});
+    else f(Shape<16, 1024>{});
 }
 template <class F>
-void backward_shape(int64_t cols, bool vec, F f) {
-    if (vec) {
-        if (cols <= 512) f(Shape<8, 8, 64>{});
-        else if (cols <= 2048) f(Shape<8, 8, 256>{});
-        else if (cols <= 4096) f(Shape<8, 8, 512>{});
-        else if (cols <= 8192) f(Shape<8, 16, 512>{});
-        else f(Shape<8, 16, 1024>{});
-    } else {
-        if (cols <= 2048) f(Shape<1, 8, 256>{});
-        else if (cols <= 8192) f(Shape<1, 16, 512>{});
-        else f(Shape<1, 16, 1024>{});
-    }
+void backward_shape(int64_t cols, F f) {
+    if (cols <= 512) f(Shape<8, 64>{});
+    else if (cols <= 2048) f(Shape<8, 256>{});
+    else if (cols <= 4096) f(Shape<8, 512>{});
+    else if (cols <= 8192) f(Shape<16, 512>{});
+    else f(Shape<16, 1024>{});
 }
 
 // Most workgroups of a backward launch: enough to fill the CUs' wave slots
 // that the kernel's registers allow, and no more, because each writes 4 rows
 // of partial sums.
-int64_t backward_wgs(int64_t rows, int64_t cols, bool vec) {
+int64_t backward_wgs(int64_t rows, int64_t cols) {
     int64_t cap = 0;
-    backward_shape(cols, vec, [&](auto sh) {
+    backward_shape(cols, [&](auto sh) {
         cap = (int64_t)kCus * 512 / decltype(sh)::THREADS;
     });
     if (cap > 2048) cap = 2048;
@@ -575,10 +556,7 @@ int block_norm_plan(const block_norm_desc_t *desc, block_norm_plan_t *out) {
         return GEMM_RS_ERR_HIP;
     }
     if (desc->backward) {
-        // the narrow kernels' rows may be cut into more workgroups
-        const int64_t a = backward_wgs(desc->rows, desc->cols, false);
-        const int64_t b = backward_wgs(desc->rows, desc->cols, true);
-        p->part_bytes = (a > b ? a : b) * 4 * desc->cols * (int64_t)sizeof(float);
+        p->part_bytes = backward_wgs(desc->rows, desc->cols) * 4 * desc->cols * (int64_t)sizeof(float);
         if (hipMalloc((void **)&p->part, p->part_bytes) != hipSuccess) {
             (void)hipGetLastError();
             free(p);
@@ -612,15 +590,15 @@ int block_norm_run(block_norm_plan_t p, const void *x, const void *y, const void
     a.x_out = x_out;
     a.u = u;
     a.u_scale = (float *)u_scale;
-    const bool vec = d.cols % 8 == 0 && wide(x, a.ld_x, se) && wide(y, a.ld_y, ye) &&
+    const bool wide_rows = d.cols % 8 == 0 && wide(x, a.ld_x, se) && wide(y, a.ld_y, ye) &&
                      wide(w_post, 8, pe) && wide(gate, 8, pe) && wide(w_pre, 8, pe) &&
                      wide(x_out, a.ld_x_out, se) && wide(u, a.ld_u, ue);
-    forward_shape(d.cols, vec, [&](auto sh) {
+    forward_shape(d.cols, [&](auto sh) {
         using S = decltype(sh);
-        const int64_t most = (int64_t)kCus * 2048 / S::THREADS;
-        launch_forward<S::VEC, S::EPT, S::THREADS>(
-            a, d.stream_dtype == GEMM_RS_F32, d.dtype == GEMM_RS_F32, d.quant != 0,
-            rows < most ? rows : most, (hipStream_t)stream);
+        const int64_t most = (int64_t)kCus * 2048 / S::THREADS, grid = rows < most ? rows : most;
+        const bool sf = d.stream_dtype == GEMM_RS_F32, yf = d.dtype == GEMM_RS_F32;
+        if (wide_rows) launch_forward<true, S::EPT, S::THREADS>(a, sf, yf, d.quant != 0, grid, (hipStream_t)stream);
+        else launch_forward<false, S::EPT, S::THREADS>(a, sf, yf, d.quant != 0, grid, (hipStream_t)stream);
     });
     return hipGetLastError() == hipSuccess ? GEMM_RS_OK : GEMM_RS_ERR_HIP;
 }
@@ -658,17 +636,18 @@ int block_norm_backward(block_norm_plan_t p, const void *dx_out, const void *du,
     a.dy = dy;
     a.dgate = (float *)dgate;
     a.part = p->part;
-    const bool vec = d.cols % 8 == 0 && wide(x_out, a.ld_x_out, se) && wide(y, a.ld_y, ye) &&
+    const bool wide_rows = d.cols % 8 == 0 && wide(x_out, a.ld_x_out, se) && wide(y, a.ld_y, ye) &&
                      wide(dx_out, a.ld_dx_out, se) && wide(du, a.ld_du, ye) &&
                      wide(w_post, 8, pe) && wide(gate, 8, pe) && wide(w_pre, 8, pe) &&
                      wide(dx, a.ld_dx, se) && wide(dy, a.ld_dy, ye) && wide(dgate, 8, 4);
-    int64_t wgs = backward_wgs(rows, d.cols, vec);
+    int64_t wgs = backward_wgs(rows, d.cols);
     a.rows_per_wg = (rows + wgs - 1) / wgs;
     wgs = (rows + a.rows_per_wg - 1) / a.rows_per_wg;
-    backward_shape(d.cols, vec, [&](auto sh) {
+    backward_shape(d.cols, [&](auto sh) {
         using S = decltype(sh);
-        launch_backward<S::VEC, S::EPT, S::THREADS>(
-            a, d.stream_dtype == GEMM_RS_F32, d.dtype == GEMM_RS_F32, wgs, s);
+        const bool sf = d.stream_dtype == GEMM_RS_F32, yf = d.dtype == GEMM_RS_F32;
+        if (wide_rows) launch_backward<true, S::EPT, S::THREADS>(a, sf, yf, wgs, s);
+        else launch_backward<false, S::EPT, S::THREADS>(a, sf, yf, wgs, s);
     });
     if (hipGetLastError() != hipSuccess) return GEMM_RS_ERR_HIP;
     // gate rows lie across workgroups' ends unless the runs are whole groups

@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "gemm_rs.h"
 
 namespace gemm_rs {
@@ -38,14 +40,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return to_bf16(a) | (to_bf16(b) << 16);
 }
 
-// VEC elements as they lie in memory: 8 elements from a 16-byte aligned
-// address, or one.  Kept raw until used, so that a row read ahead costs the
-// registers of its storage type only.
-template <bool F32, int VEC> struct Raw;
-template <> struct Raw<true, 8> { u32x4_t a, b; };
-template <> struct Raw<false, 8> { u32x4_t a; };
-template <> struct Raw<true, 1> { float a; };
-template <> struct Raw<false, 1> { uint16_t a; };
+// 8 elements as they lie in memory, kept raw until used, so that a row read
+// ahead costs the registers of its storage type only.
+template <bool F32> struct Raw;
+template <> struct Raw<true> { u32x4_t a, b; };
+template <> struct Raw<false> { u32x4_t a; };
 
 // Row `row` of a matrix of `elem`-byte elements: a wave-uniform address, which
 // a 32-bit column number per lane is added to.
@@ -56,58 +55,84 @@ __device__ __forceinline__ void *row_of(void *p, int64_t row, int64_t ld, int el
     return (char *)p + row * ld * elem;
 }
 
-template <bool F32, int VEC>
-__device__ __forceinline__ void load_raw(Raw<F32, VEC> &r, const void *p, uint32_t i) {
-    if constexpr (VEC == 8 && F32) {
-        const u32x4_t *q = (const u32x4_t *)((const float *)p + i);
-        r.a = q[0];
-        r.b = q[1];
-    } else if constexpr (VEC == 8) {
-        r.a = *(const u32x4_t *)((const uint16_t *)p + i);
-    } else if constexpr (F32) {
-        r.a = ((const float *)p)[i];
+// Columns c..c+7 of a row of `cols` (c < cols).  WIDE: the row starts on 16
+// bytes and cols is a multiple of 8.  Otherwise rows start on any element: the
+// same 16-byte accesses, which the hardware takes at any address, and the
+// row's last few columns one by one (the rest of them read as zero).
+typedef u32x4_t u32x4_at4_t __attribute__((aligned(4)));
+typedef u32x4_t u32x4_at2_t __attribute__((aligned(2)));
+typedef u32x2_t u32x2_at1_t __attribute__((aligned(1)));
+
+template <bool F32, bool WIDE>
+__device__ __forceinline__ void load8(Raw<F32> &r, const void *row, uint32_t c, uint32_t cols) {
+    if (WIDE || c + 8 <= cols) {
+        if constexpr (F32) {
+            typedef std::conditional_t<WIDE, u32x4_t, u32x4_at4_t> words;
+            const words *q = (const words *)((const float *)row + c);
+            r.a = q[0];
+            r.b = q[1];
+        } else {
+            typedef std::conditional_t<WIDE, u32x4_t, u32x4_at2_t> words;
+            r.a = *(const words *)((const uint16_t *)row + c);
+        }
     } else {
-        r.a = ((const uint16_t *)p)[i];
+        r = Raw<F32>{};
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (c + e < cols) {
+                if constexpr (F32) {
+                    const uint32_t w = ((const uint32_t *)row)[c + e];
+                    if (e < 4) r.a[e] = w;
+                    else r.b[e - 4] = w;
+                } else {
+                    r.a[e >> 1] |= (uint32_t)((const uint16_t *)row)[c + e] << (16 * (e & 1));
+                }
+            }
     }
 }
 
-template <bool F32, int VEC>
-__device__ __forceinline__ float raw_at(const Raw<F32, VEC> &r, int e) {
-    if constexpr (VEC == 8 && F32)
-        return __uint_as_float(e < 4 ? r.a[e] : r.b[e - 4]);
-    else if constexpr (VEC == 8)
-        return (e & 1) ? bf16_hi(r.a[e >> 1]) : bf16_lo(r.a[e >> 1]);
-    else if constexpr (F32)
-        return r.a;
-    else
-        return bf16_lo(r.a);
+template <bool F32>
+__device__ __forceinline__ float raw_at(const Raw<F32> &r, int e) {
+    if constexpr (F32) return __uint_as_float(e < 4 ? r.a[e] : r.b[e - 4]);
+    else return (e & 1) ? bf16_hi(r.a[e >> 1]) : bf16_lo(r.a[e >> 1]);
 }
 
-template <bool F32, int VEC, bool STREAM = false>
-__device__ __forceinline__ void store_vec(void *p, uint32_t i, const float *v) {
-    if constexpr (VEC == 8 && F32) {
-        f32x4_t *q = (f32x4_t *)((float *)p + i);
-        const f32x4_t a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
-        if constexpr (STREAM) {
-            __builtin_nontemporal_store(a, q);
-            __builtin_nontemporal_store(b, q + 1);
+// The same columns written; STREAM: past the caches.
+template <bool F32, bool WIDE, bool STREAM = false>
+__device__ __forceinline__ void store8(void *row, uint32_t c, uint32_t cols, const float *v) {
+    if (WIDE || c + 8 <= cols) {
+        if constexpr (F32) {
+            typedef std::conditional_t<WIDE, u32x4_t, u32x4_at4_t> words;
+            words *q = (words *)((float *)row + c);
+            u32x4_t a, b;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                a[e] = __float_as_uint(v[e]);
+                b[e] = __float_as_uint(v[e + 4]);
+            }
+            if constexpr (STREAM) {
+                __builtin_nontemporal_store(a, q);
+                __builtin_nontemporal_store(b, q + 1);
+            } else {
+                q[0] = a;
+                q[1] = b;
+            }
         } else {
-            q[0] = a;
-            q[1] = b;
+            typedef std::conditional_t<WIDE, u32x4_t, u32x4_at2_t> words;
+            words *q = (words *)((uint16_t *)row + c);
+            u32x4_t w;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+            if constexpr (STREAM) __builtin_nontemporal_store(w, q);
+            else *q = w;
         }
-    } else if constexpr (VEC == 8) {
-        u32x4_t w;
-        w[0] = pack_bf16(v[0], v[1]);
-        w[1] = pack_bf16(v[2], v[3]);
-        w[2] = pack_bf16(v[4], v[5]);
-        w[3] = pack_bf16(v[6], v[7]);
-        u32x4_t *q = (u32x4_t *)((uint16_t *)p + i);
-        if constexpr (STREAM) __builtin_nontemporal_store(w, q);
-        else *q = w;
-    } else if constexpr (F32) {
-        ((float *)p)[i] = v[0];
     } else {
-        ((uint16_t *)p)[i] = (uint16_t)to_bf16(v[0]);
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (c + e < cols) {
+                if constexpr (F32) ((float *)row)[c + e] = v[e];
+                else ((uint16_t *)row)[c + e] = (uint16_t)to_bf16(v[e]);
+            }
     }
 }
 
@@ -199,6 +224,21 @@ __device__ __forceinline__ int quant_one(const QuantRow &r, float x) {
     if (!r.finite) return 0;
     // |x * inv| <= 127 up to rounding, which rint takes back to 127
     return (int)rintf(x * r.pre * r.inv);
+}
+// Columns c..c+7 of a row of `cols` bytes, from at(e).
+template <bool WIDE, class F>
+__device__ __forceinline__ void quant8(const QuantRow &q, int8_t *row, uint32_t c, uint32_t cols, F at) {
+    if (WIDE || c + 8 <= cols) {
+        typedef std::conditional_t<WIDE, u32x2_t, u32x2_at1_t> words;
+        u32x2_t w = {0u, 0u};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e >> 2] |= (uint32_t)(quant_one(q, at(e)) & 0xff) << (8 * (e & 3));
+        *(words *)(row + c) = w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 7; ++e)
+            if (c + e < cols) row[c + e] = (int8_t)quant_one(q, at(e));
+    }
 }
 
 }  // namespace ffn

@@ -199,28 +199,28 @@ __global__ __launch_bounds__(256) void grouped_narrow_kernel(GroupedArgs p) {
 // size, is stored past them (6001 rows, 32 experts of 2048 x 1792 in 32 bits:
 // 165 us, streamed 129).
 template <bool STREAM>
-__device__ __forceinline__ void store8(const GroupedArgs &p, int64_t row, int64_t n, const int (&v)[8]) {
+__device__ __forceinline__ void store_run(const GroupedArgs &p, int64_t row, int64_t n, const int (&v)[8]) {
     float x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = __int_as_float(v[e]);
-    const uint32_t at = (uint32_t)n;
+    const uint32_t at = (uint32_t)n, cols = (uint32_t)p.N;
     void *const C = row_of(p.C, row, p.ldc, p.out_f32 ? 4 : 2);
     if (p.out_f32) {
         if (p.accumulate) {
-            Raw<true, 8> c;
-            load_raw(c, C, at);
+            Raw<true> c;
+            load8<true, true>(c, C, at, cols);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] += raw_at(c, e);
         }
-        store_vec<true, 8, STREAM>(C, at, x);
+        store8<true, true, STREAM>(C, at, cols, x);
     } else {
         if (p.accumulate) {
-            Raw<false, 8> c;
-            load_raw(c, C, at);
+            Raw<false> c;
+            load8<false, true>(c, C, at, cols);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] += raw_at(c, e);
         }
-        store_vec<false, 8, STREAM>(C, at, x);
+        store8<false, true, STREAM>(C, at, cols, x);
     }
 }
 
@@ -278,7 +278,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_tile_kernel(GroupedArg
         const Operand b = {(const char *)(p.B + (int64_t)lo * p.ldb + n0), p.ldb * 2, n_left * 2};
         tile.template run<2>(smem, a, b, hi - lo);
         tile.template store<8>(smem, [&](int r, int c, const int (&v)[8]) {
-            if (r < m_left && c < n_left) store8<true>(out, (int64_t)e * p.K + m0 + r, n0 + c, v);
+            if (r < m_left && c < n_left) store_run<true>(out, (int64_t)e * p.K + m0 + r, n0 + c, v);
         });
     } else {
         RowTile t;
@@ -288,7 +288,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_tile_kernel(GroupedArg
         const int32_t n_left = (int32_t)(p.N - n0 < BN ? p.N - n0 : BN);
         tile.template run<2>(smem, row_operand(p, t, m_left), column_operand<OP>(p, t.e, n0, n_left), (int32_t)p.K);
         tile.template store<8>(smem, [&](int r, int c, const int (&v)[8]) {
-            if (r < m_left && c < n_left) store8<false>(p, (int64_t)t.row0 + r, n0 + c, v);
+            if (r < m_left && c < n_left) store_run<false>(p, (int64_t)t.row0 + r, n0 + c, v);
         });
     }
 }
@@ -432,7 +432,7 @@ __global__ __launch_bounds__(NW * 64) void grouped_stream_kernel(GroupedArgs p) 
     const int32_t n_left = (int32_t)(p.N - n0 < BN ? p.N - n0 : BN);
     T::run((lds_t *)smem_generic, row_operand(p, t, m_left), column_operand<OP>(p, t.e, n0, n_left),
            (int32_t)p.K, [&](int r, int c, const int (&v)[8]) {
-               if (r < m_left && c < n_left) store8<false>(p, (int64_t)t.row0 + r, n0 + c, v);
+               if (r < m_left && c < n_left) store_run<false>(p, (int64_t)t.row0 + r, n0 + c, v);
            });
 }
 
@@ -462,15 +462,15 @@ __global__ __launch_bounds__(256) void grouped_join_kernel(GroupedArgs p) {
         const int64_t row = i / runs, n = i % runs * 8;
         float x[8] = {};
         for (int s = 0; s < p.parts; ++s) {
-            Raw<true, 8> r;
-            load_raw(r, p.slots + ((int64_t)s * p.E * p.K + row) * p.N, (uint32_t)n);
+            Raw<true> r;
+            load8<true, true>(r, p.slots + ((int64_t)s * p.E * p.K + row) * p.N, (uint32_t)n, (uint32_t)p.N);
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] += raw_at(r, e);
         }
         int v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = __float_as_int(x[e]);
-        store8<false>(p, row, n, v);
+        store_run<false>(p, row, n, v);
     }
 }
 

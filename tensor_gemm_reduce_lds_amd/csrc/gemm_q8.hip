@@ -65,8 +65,9 @@ __global__ __launch_bounds__(64 * WGM * WGN) void q8_tile_kernel(Q8Args p) {
             float x[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] = scaled(v[e], sa, sw[e], p.bias ? &bias[e] : nullptr);
-            if (p.out_f32) store_vec<true, 8>(row_of(p.D, m, p.ldd, 4), (uint32_t)(n0 + c), x);
-            else store_vec<false, 8>(row_of(p.D, m, p.ldd, 2), (uint32_t)(n0 + c), x);
+            const uint32_t at = (uint32_t)(n0 + c), cols = (uint32_t)p.N;
+            if (p.out_f32) store8<true, true>(row_of(p.D, m, p.ldd, 4), at, cols, x);
+            else store8<false, true>(row_of(p.D, m, p.ldd, 2), at, cols, x);
         });
     } else {
         const int c1 = (int)threadIdx.x % BN;
@@ -190,44 +191,33 @@ __global__ __launch_bounds__(NW * 64) void q8_rows_kernel(Q8Args p) {
 
 // Rows of up to EPT * THREADS columns, one per workgroup, in registers; EPT
 // 0: rows of any length, read twice (the second time from the caches).
-template <bool F32, int VEC, int EPT, int THREADS>
-__global__ __launch_bounds__(THREADS) void quantize_kernel(const void *x, int64_t rows, int64_t cols,
+template <bool F32, bool WIDE, int EPT, int THREADS>
+__global__ __launch_bounds__(THREADS) void quantize_kernel(const void *x, int64_t rows, uint32_t cols,
                                                            int64_t ldx, int8_t *q, int64_t ldq,
                                                            float *scale) {
     __shared__ float slots[2 * 16];
     int turn = 0;
-    const int64_t padded = (cols + 15) / 16 * 16;
-    constexpr int VPT = EPT ? EPT / VEC : 1;
-    const int64_t t0 = (int64_t)threadIdx.x * VEC;
-    auto put = [&](const QuantRow &k, const Raw<F32, VEC> &r, int8_t *to) {
-        if constexpr (VEC == 8) {
-            u32x2_t w = {0u, 0u};
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                w[e >> 2] |= (uint32_t)(quant_one(k, raw_at(r, e)) & 0xff) << (8 * (e & 3));
-            *(u32x2_t *)to = w;
-        } else {
-            *to = (int8_t)quant_one(k, raw_at(r, 0));
-        }
-    };
+    const uint32_t padded = (cols + 15) / 16 * 16, t0 = threadIdx.x * 8;
+    constexpr int VPT = EPT ? EPT / 8 : 1;
     for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
-        Raw<F32, VEC> held[VPT];
+        const void *const from = row_of(x, row, ldx, F32 ? 4 : 2);
+        Raw<F32> held[VPT];
         float m[1] = {0.0f};
-        auto take = [&](Raw<F32, VEC> &r, int64_t c) {
-            r = Raw<F32, VEC>{};
-            if (c < cols) load_raw(r, row_of(x, row, ldx, F32 ? 4 : 2), (uint32_t)c);
+        auto take = [&](Raw<F32> &r, uint32_t c) {
+            r = Raw<F32>{};
+            if (c < cols) load8<F32, WIDE>(r, from, c, cols);
         };
-        auto look = [&](const Raw<F32, VEC> &r) {
+        auto look = [&](const Raw<F32> &r) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) m[0] = MaxBits::join(m[0], fabsf(raw_at(r, e)));
+            for (int e = 0; e < 8; ++e) m[0] = MaxBits::join(m[0], fabsf(raw_at(r, e)));
         };
         if constexpr (EPT) {
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) take(held[k], t0 + k * THREADS * VEC);
+            for (int k = 0; k < VPT; ++k) take(held[k], t0 + k * THREADS * 8);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) look(held[k]);
         } else {
-            for (int64_t c = t0; c < cols; c += THREADS * VEC) {
+            for (uint32_t c = t0; c < cols; c += THREADS * 8) {
                 take(held[0], c);
                 look(held[0]);
             }
@@ -236,16 +226,17 @@ __global__ __launch_bounds__(THREADS) void quantize_kernel(const void *x, int64_
         const QuantRow k = quant_row(m[0]);
         if (threadIdx.x == 0) scale[row] = k.scale;
         int8_t *const to = q + row * ldq;
+        // (the padding is whole runs of 8)
+        auto put = [&](const Raw<F32> &r, uint32_t c) {
+            if (c < padded) quant8<WIDE>(k, to, c, padded, [&](int e) { return raw_at(r, e); });
+        };
         if constexpr (EPT) {
 #pragma unroll
-            for (int i = 0; i < VPT; ++i) {
-                const int64_t c = t0 + i * THREADS * VEC;
-                if (c < padded) put(k, held[i], to + c);
-            }
+            for (int i = 0; i < VPT; ++i) put(held[i], t0 + i * THREADS * 8);
         } else {
-            for (int64_t c = t0; c < padded; c += THREADS * VEC) {
+            for (uint32_t c = t0; c < padded; c += THREADS * 8) {
                 take(held[0], c);
-                put(k, held[0], to + c);
+                put(held[0], c);
             }
         }
     }
@@ -385,20 +376,20 @@ int gemm_q8_quantize(const void *x, int32_t dtype, int64_t rows, int64_t cols, i
     const bool vec = cols % 8 == 0 && ldx % 8 == 0 && ldq % 8 == 0 && aligned(x, 16) && aligned(q, 8);
     const dim3 grid((unsigned)(rows < 65536 ? rows : 65536));
     auto go = [&](auto *kernel, int threads) {
-        hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, (hipStream_t)stream, x, rows, cols, ldx,
+        hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, (hipStream_t)stream, x, rows, (uint32_t)cols, ldx,
                            (int8_t *)q, ldq, (float *)scale);
     };
-    auto of_type = [&](auto f32) {
-        constexpr bool F = decltype(f32)::value;
-        if (!vec) go(quantize_kernel<F, 1, 0, 256>, 256);
-        else if (cols <= 2048 && rows >= kCus) go(quantize_kernel<F, 8, 32, 64>, 64);
-        else if (cols <= 2048) go(quantize_kernel<F, 8, 8, 256>, 256);
-        else if (cols <= 8192) go(quantize_kernel<F, 8, 16, 512>, 512);
-        else if (cols <= 16384) go(quantize_kernel<F, 8, 16, 1024>, 1024);
-        else go(quantize_kernel<F, 8, 0, 256>, 256);
+    auto of_type = [&](auto f32, auto wide) {
+        constexpr bool F = decltype(f32)::value, W = decltype(wide)::value;
+        // a wave per row where there are many short rows, else a workgroup
+        if (cols <= 2048 && rows >= kCus) go(quantize_kernel<F, W, 32, 64>, 64);
+        else if (cols <= 2048) go(quantize_kernel<F, W, 8, 256>, 256);
+        else if (cols <= 8192) go(quantize_kernel<F, W, 16, 512>, 512);
+        else if (cols <= 16384) go(quantize_kernel<F, W, 16, 1024>, 1024);
+        else go(quantize_kernel<F, W, 0, 256>, 256);
     };
-    if (dtype == GEMM_RS_F32) of_type(std::true_type{});
-    else of_type(std::false_type{});
+    if (dtype == GEMM_RS_F32) vec ? of_type(std::true_type{}, std::true_type{}) : of_type(std::true_type{}, std::false_type{});
+    else vec ? of_type(std::false_type{}, std::true_type{}) : of_type(std::false_type{}, std::false_type{});
     return hipGetLastError() == hipSuccess ? GEMM_RS_OK : GEMM_RS_ERR_HIP;
 }
 
