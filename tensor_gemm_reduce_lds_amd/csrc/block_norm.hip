@@ -1,15 +1,19 @@
 // Norms before and after a block with gate and residual scale (block_norm.h).
 //
-// Forward: one workgroup per row at a time, the whole row in registers: one
-// read of x and y, one write of x' and u.  Two joins over the workgroup (the
-// mean square of y, then of x', which needs the first), a third for the
-// largest |u| when u is quantised.
+// Bound by memory (by latency for few rows).  Forward: one workgroup per row
+// at a time, the whole row in registers: one read of x and y, one write of x'
+// and u.  Two joins over the workgroup (the mean square of y, then of x', which
+// needs the first), a third for the largest |u| when u is quantised.
+// 8000 x 8192, f32 stream: 148 us, 5.3 TB/s (a large copy on the same card runs
+// at 4.95 TB/s).
 //
-// Backward: a workgroup walks a run of consecutive rows and keeps the sums
-// for dw_post, dw_pre and dgate of its columns in registers; two joins per
-// row (mean squares of x' and y and the product a.x' together, then b.y).
-// The partial sums go to the workspace once per workgroup and a second
-// kernel adds them in a fixed order.
+// Backward: a workgroup walks a run of consecutive rows, loading one row while
+// it works on the one before, and keeps the sums for dw_post, dw_pre and
+// dgate of its columns in registers; two joins per row (mean squares of x' and
+// y and the product a.x' together, then b.y).  The partial sums go to the
+// workspace once per workgroup and a second kernel adds them in a fixed order.
+// 8192 x 8192 bf16: 180 us, 4.5 TB/s; 1000 x 4096, f32 stream: 25 us (few rows
+// per workgroup, and the partial sums are a third of the traffic).
 #include <math.h>
 #include <stdlib.h>
 
@@ -164,6 +168,29 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
     }
 }
 
+// EPT floats of a thread, in registers, or in LDS where a workgroup's rows take
+// all registers (16-byte pieces, neighbouring threads' next to each other).
+template <int EPT, int THREADS, bool LDS>
+struct Own {
+    float v[EPT];
+    static constexpr int BYTES = 0;
+    __device__ __forceinline__ void place(char *) {}
+    __device__ __forceinline__ float get(int i) const { return v[i]; }
+    __device__ __forceinline__ void set(int i, float x) { v[i] = x; }
+};
+template <int EPT, int THREADS>
+struct Own<EPT, THREADS, true> {
+    f32x4_t *at;
+    static constexpr int BYTES = EPT * THREADS * 4;
+    __device__ __forceinline__ void place(char *p) { at = (f32x4_t *)p + threadIdx.x; }
+    __device__ __forceinline__ float get(int i) const { return at[i / 4 * THREADS][i % 4]; }
+    __device__ __forceinline__ void set(int i, float x) { at[i / 4 * THREADS][i % 4] = x; }
+};
+// Rows of more than 8192 columns keep w_pre and the sums for dw_post in LDS
+// (8192 x 16384 bf16: 1449 us with all in registers and spills, 471).
+template <int EPT, int THREADS>
+constexpr bool kOwnInLds = EPT * THREADS > 8192;
+
 // A row's inputs of the backward, as they lie in memory.
 template <int VPT, bool SF, bool YF>
 struct BackwardRow {
@@ -187,21 +214,28 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
     // gw: gate * w_post.  Summed over rows: D * yh since the last change of
     // gate row (dgate is that times w_post, and gate times that goes into
     // dw_post), and du * xh.
-    float w_pre[EPT], gw[EPT], s_dy[EPT], s_post[EPT], s_pre[EPT];
+    constexpr bool LDS = kOwnInLds<EPT, THREADS>;
+    extern __shared__ __attribute__((aligned(16))) char own[];
+    Own<EPT, THREADS, LDS> w_pre, s_post;
+    w_pre.place(own);
+    s_post.place(own + w_pre.BYTES);
+    float gw[EPT], s_dy[EPT], s_pre[EPT];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
-        float *wo = gw + k * 8, *wp = w_pre + k * 8;
+        float *wo = gw + k * 8, wp[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int i = k * 8 + e;
             wo[e] = wp[e] = 1.0f;
-            s_dy[i] = s_post[i] = s_pre[i] = 0.0f;
+            s_dy[k * 8 + e] = s_pre[k * 8 + e] = 0.0f;
+            s_post.set(k * 8 + e, 0.0f);
         }
         if (c < cols) {
             if (a.post) load_param<WIDE>(a, a.w_post, c, a.weight_offset, wo);
             if (a.pre) load_param<WIDE>(a, a.w_pre, c, a.weight_offset, wp);
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w_pre.set(k * 8 + e, wp[e]);
     }
     auto take = [&](Row &r, int64_t row) __attribute__((always_inline)) {
 #pragma unroll
@@ -242,7 +276,7 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 float &s = s_dy[k * 8 + e];
-                s_post[k * 8 + e] += g[e] * s;
+                s_post.set(k * 8 + e, s_post.get(k * 8 + e) + g[e] * s);
                 w[e] *= s;
                 s = 0.0f;
             }
@@ -289,7 +323,7 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
                 const int i = k * 8 + e;
                 const float x = raw_at(r.x[k], e), y = raw_at(r.y[k], e);
                 s[0] += x * x;
-                s[1] += raw_at(r.u[k], e) * w_pre[i] * x;
+                s[1] += raw_at(r.u[k], e) * w_pre.get(i) * x;
                 s[2] += y * y;
             }
         block_join<Sum, THREADS, 3>(s, slots, turn);
@@ -307,7 +341,7 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
                 const int i = k * 8 + e;
                 const float xh = raw_at(r.x[k], e) * r1, du = raw_at(r.u[k], e);
                 float d = raw_at(r.d[k], e);
-                if (a.pre) d += r1 * (du * w_pre[i] - xh * m1);
+                if (a.pre) d += r1 * (du * w_pre.get(i) - xh * m1);
                 s_pre[i] += du * xh;
                 dx[e] = a.has_y ? a.res_scale * d : d;
                 const float yh = raw_at(r.y[k], e) * r2;
@@ -337,14 +371,17 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
         if (gate_row >= 0) end_gate();
     } else {
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) s_post[i] = s_dy[i];
+        for (int i = 0; i < EPT; ++i) s_post.set(i, s_dy[i]);
     }
     float *part = a.part + (int64_t)blockIdx.x * 4 * a.cols;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
         const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
         if (c >= cols) continue;
-        if (a.post) store8<true, WIDE>(part, c, cols, s_post + k * 8);
+        float sp[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sp[e] = s_post.get(k * 8 + e);
+        if (a.post) store8<true, WIDE>(part, c, cols, sp);
         if (a.pre) store8<true, WIDE>(part + a.cols, c, cols, s_pre + k * 8);
     }
 }
@@ -421,15 +458,13 @@ void launch_forward(const NormArgs &a, bool sf, bool yf, bool quant, int64_t gri
 }
 
 template <bool WIDE, int EPT, int THREADS>
-void launch_backward(const NormArgs &a, bool sf, bool yf, int64_t grid, hipStream_t s) {
-    auto go = [&](auto *kernel) {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(THREADS), 0, s, a);
-    };
-    constexpr bool AHEAD = EPT == 8 || THREADS < 1024;
-    if (sf && yf) go(norm_backward_kernel<WIDE, EPT, THREADS, true, true, AHEAD>);
-    else if (sf) go(norm_backward_kernel<WIDE, EPT, THREADS, true, false, AHEAD>);
-    else if (yf) go(norm_backward_kernel<WIDE, EPT, THREADS, false, true, AHEAD>);
-    else go(norm_backward_kernel<WIDE, EPT, THREADS, false, false, AHEAD>);
+hipError_t launch_backward(const NormArgs &a, bool sf, bool yf, int64_t grid, hipStream_t s) {
+    constexpr bool AHEAD = !kOwnInLds<EPT, THREADS>;    // no registers for it there
+    constexpr int lds = 2 * Own<EPT, THREADS, kOwnInLds<EPT, THREADS>>::BYTES;
+    if (sf && yf) return launch_lds<norm_backward_kernel<WIDE, EPT, THREADS, true, true, AHEAD>>(grid, THREADS, lds, s, a);
+    if (sf) return launch_lds<norm_backward_kernel<WIDE, EPT, THREADS, true, false, AHEAD>>(grid, THREADS, lds, s, a);
+    if (yf) return launch_lds<norm_backward_kernel<WIDE, EPT, THREADS, false, true, AHEAD>>(grid, THREADS, lds, s, a);
+    return launch_lds<norm_backward_kernel<WIDE, EPT, THREADS, false, false, AHEAD>>(grid, THREADS, lds, s, a);
 }
 
 // Threads of a workgroup and columns of a row per thread.
@@ -438,22 +473,27 @@ struct Shape {
     static constexpr int EPT = EPT_, THREADS = THREADS_;
 };
 
-// Calls f with the kernel shape of a row length.
+// Calls f with the kernel shape of a row length.  Up to 8192 columns: few rows
+// take 1024 threads (the latency of one row), many take 512, which leaves each
+// CU rows to overlap (8192 x 8192 bf16: 115 / 102 us).
 template <class F>
-void forward_shape(int64_t cols, F f) {
+void forward_shape(int64_t rows, int64_t cols, F f) {
     if (cols <= 512) f(Shape<8, 64>{});
+    else if (cols <= 1024) f(Shape<8, 128>{});
     else if (cols <= 2048) f(Shape<8, 256>{});
     else if (cols <= 4096) f(Shape<8, 512>{});
-    else if (cols <= 8192) f(Shape<8, 1024>{});
+    else if (cols <= 8192 && rows < kCus) f(Shape<8, 1024>{});
+    else if (cols <= 8192) f(Shape<16, 512>{});
     else f(Shape<16, 1024>{});
 }
 template <class F>
 void backward_shape(int64_t cols, F f) {
     if (cols <= 512) f(Shape<8, 64>{});
+    else if (cols <= 1024) f(Shape<8, 128>{});
     else if (cols <= 2048) f(Shape<8, 256>{});
     else if (cols <= 4096) f(Shape<8, 512>{});
     else if (cols <= 8192) f(Shape<16, 512>{});
-    else f(Shape<16, 1024>{});
+    else f(Shape<32, 512>{});
 }
 
 // Most workgroups of a backward launch: enough to fill the CUs' wave slots
@@ -593,7 +633,7 @@ int block_norm_run(block_norm_plan_t p, const void *x, const void *y, const void
     const bool wide_rows = d.cols % 8 == 0 && wide(x, a.ld_x, se) && wide(y, a.ld_y, ye) &&
                      wide(w_post, 8, pe) && wide(gate, 8, pe) && wide(w_pre, 8, pe) &&
                      wide(x_out, a.ld_x_out, se) && wide(u, a.ld_u, ue);
-    forward_shape(d.cols, [&](auto sh) {
+    forward_shape(rows, d.cols, [&](auto sh) {
         using S = decltype(sh);
         const int64_t most = (int64_t)kCus * 2048 / S::THREADS, grid = rows < most ? rows : most;
         const bool sf = d.stream_dtype == GEMM_RS_F32, yf = d.dtype == GEMM_RS_F32;
@@ -643,13 +683,14 @@ int block_norm_backward(block_norm_plan_t p, const void *dx_out, const void *du,
     int64_t wgs = backward_wgs(rows, d.cols);
     a.rows_per_wg = (rows + wgs - 1) / wgs;
     wgs = (rows + a.rows_per_wg - 1) / a.rows_per_wg;
+    hipError_t e = hipSuccess;
     backward_shape(d.cols, [&](auto sh) {
         using S = decltype(sh);
         const bool sf = d.stream_dtype == GEMM_RS_F32, yf = d.dtype == GEMM_RS_F32;
-        if (wide_rows) launch_backward<true, S::EPT, S::THREADS>(a, sf, yf, wgs, s);
-        else launch_backward<false, S::EPT, S::THREADS>(a, sf, yf, wgs, s);
+        e = wide_rows ? launch_backward<true, S::EPT, S::THREADS>(a, sf, yf, wgs, s)
+                      : launch_backward<false, S::EPT, S::THREADS>(a, sf, yf, wgs, s);
     });
-    if (hipGetLastError() != hipSuccess) return GEMM_RS_ERR_HIP;
+    if (e != hipSuccess) return GEMM_RS_ERR_HIP;
     // gate rows lie across workgroups' ends unless the runs are whole groups
     const bool split = gated && wgs > 1 && a.rows_per_wg % a.rows_per_gate != 0;
     if (d.post || d.pre || split) {

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
 #include <type_traits>
 
 #include "gemm_rs.h"
@@ -239,6 +240,25 @@ __device__ __forceinline__ void quant8(const QuantRow &q, int8_t *row, uint32_t 
         for (int e = 0; e < 7; ++e)
             if (c + e < cols) row[c + e] = (int8_t)quant_one(q, at(e));
     }
+}
+
+// Launches a kernel with dynamic LDS, whose limit is a per-device attribute of
+// the kernel: set once per device (thread-safe).
+template <auto KERNEL, class ARGS>
+inline hipError_t launch_lds(int64_t blocks, int threads, int lds_bytes, hipStream_t s, const ARGS &a) {
+    constexpr int kMaxDevices = 64;
+    static std::once_flag once[kMaxDevices];
+    static hipError_t set[kMaxDevices];
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices)
+        return hipErrorInvalidDevice;
+    std::call_once(once[dev], [dev, lds_bytes] {
+        set[dev] = hipFuncSetAttribute((const void *)KERNEL,
+                                       hipFuncAttributeMaxDynamicSharedMemorySize, lds_bytes);
+    });
+    if (set[dev] != hipSuccess) return set[dev];
+    hipLaunchKernelGGL(KERNEL, dim3((unsigned)blocks), dim3(threads), lds_bytes, s, a);
+    return hipGetLastError();
 }
 
 }  // namespace ffn

@@ -19,7 +19,6 @@
 // stored.
 #pragma once
 
-#include <mutex>
 #include <type_traits>
 #include <utility>
 
@@ -459,25 +458,6 @@ struct Tile {
         }
     }
 };
-
-// Launches a kernel with dynamic LDS, whose limit is a per-device attribute of
-// the kernel: set once per device (thread-safe).
-template <auto KERNEL, class ARGS>
-inline hipError_t launch_lds(int64_t blocks, int threads, int lds_bytes, hipStream_t s, const ARGS &a) {
-    constexpr int kMaxDevices = 64;
-    static std::once_flag once[kMaxDevices];
-    static hipError_t set[kMaxDevices];
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices)
-        return hipErrorInvalidDevice;
-    std::call_once(once[dev], [dev, lds_bytes] {
-        set[dev] = hipFuncSetAttribute((const void *)KERNEL,
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, lds_bytes);
-    });
-    if (set[dev] != hipSuccess) return set[dev];
-    hipLaunchKernelGGL(KERNEL, dim3((unsigned)blocks), dim3(threads), lds_bytes, s, a);
-    return hipGetLastError();
-}
 
 }  // namespace ffn
 }  // namespace gemm_rs
