@@ -255,10 +255,13 @@ hipError_t launch_rows(const Q8Args &q, hipStream_t s) {
     return launch_lds<q8_rows_kernel<MB, NB, NW, S>>((q.N + NB * 16 - 1) / (NB * 16), NW * 64, R::LDS_BYTES, s, q);
 }
 
-// Up to 128 rows the product is bound by streaming w: as many workgroups as
+// Up to 64 rows the product is bound by streaming w: as many workgroups as
 // there are CUs, so 32 channels each where that still makes 256 of them (the
 // rows of a are then read half as often), else 16.  Measured, us for 16 / 32
-// channels: 64 x 8192 x 3584 11.7 / 9.7, 64 x 3584 x 8192 10.5 / 14.1.
+// channels: 64 x 8192 x 3584 11.7 / 9.7, 64 x 3584 x 8192 10.5 / 14.1.  From 65
+// rows on the tiles are as fast or faster (128 rows in such streams against
+// 64 x 64 tiles: 128 x 8192 x 3584 14.6 / 11.5, 128 x 3584 x 8192 17.8 / 18.6,
+// 71 x 5241 x 6656 26.4 / 17.6; 64 rows: 64 x 3584 x 8192 10.4 / 18.2).
 template <int MB, int NW1, int S1, int NW2, int S2>
 hipError_t launch_few(const Q8Args &q, hipStream_t s) {
     if (q.N >= 32 * kCus) return launch_rows<MB, 2, NW2, S2>(q, s);
@@ -269,7 +272,6 @@ hipError_t launch_product(const Q8Args &q, hipStream_t s) {
     if (q.M <= 16) return launch_few<1, 8, 4, 8, 3>(q, s);
     if (q.M <= 32) return launch_few<2, 8, 3, 8, 2>(q, s);
     if (q.M <= 64) return launch_few<4, 8, 2, 4, 3>(q, s);
-    if (q.M <= 128) return launch_few<8, 4, 2, 4, 2>(q, s);
     // The tile with the least time, from the rounds of 256 workgroups that it
     // makes (a round costs about as much where it is not full) and times
     // measured at K = 3584, in us.  Large tiles read fewer bytes per operation,
