@@ -5,7 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <mutex>
+#include <atomic>
 #include <type_traits>
 
 #include "gemm_rs.h"
@@ -243,20 +243,20 @@ __device__ __forceinline__ void quant8(const QuantRow &q, int8_t *row, uint32_t 
 }
 
 // Launches a kernel with dynamic LDS, whose limit is a per-device attribute of
-// the kernel: set once per device (thread-safe).
+// the kernel: set on the first launch there (threads that race set it twice).
 template <auto KERNEL, class ARGS>
 inline hipError_t launch_lds(int64_t blocks, int threads, int lds_bytes, hipStream_t s, const ARGS &a) {
     constexpr int kMaxDevices = 64;
-    static std::once_flag once[kMaxDevices];
-    static hipError_t set[kMaxDevices];
+    static std::atomic<bool> set[kMaxDevices];
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices)
         return hipErrorInvalidDevice;
-    std::call_once(once[dev], [dev, lds_bytes] {
-        set[dev] = hipFuncSetAttribute((const void *)KERNEL,
-                                       hipFuncAttributeMaxDynamicSharedMemorySize, lds_bytes);
-    });
-    if (set[dev] != hipSuccess) return set[dev];
+    if (!set[dev].load(std::memory_order_acquire)) {
+        const hipError_t e = hipFuncSetAttribute((const void *)KERNEL,
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, lds_bytes);
+        if (e != hipSuccess) return e;
+        set[dev].store(true, std::memory_order_release);
+    }
     hipLaunchKernelGGL(KERNEL, dim3((unsigned)blocks), dim3(threads), lds_bytes, s, a);
     return hipGetLastError();
 }

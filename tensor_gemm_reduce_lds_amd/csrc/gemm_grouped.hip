@@ -57,8 +57,8 @@ __device__ __forceinline__ void check_offsets(const GroupedArgs &p) {
 
 struct RowTile {
     int e;
-    int32_t lo, hi;     // the expert's rows
     int32_t row0;       // the tile's first row
+    int32_t end;        // past the expert's last row
     int tn;             // column tile
 };
 
@@ -102,13 +102,13 @@ __device__ __forceinline__ bool find_row_tile(const GroupedArgs &p, int bm, uint
             // a tile is left out, every other lies inside its expert
             if (j >= n * tn) return false;
             t->e = __builtin_amdgcn_readfirstlane(e0 + src);
-            group_rows(p, t->e, &t->lo, &t->hi);
-            t->lo = __builtin_amdgcn_readfirstlane(t->lo);
-            t->hi = __builtin_amdgcn_readfirstlane(t->hi);
+            int32_t lo, hi;
+            group_rows(p, t->e, &lo, &hi);
+            t->end = __builtin_amdgcn_readfirstlane(hi);
             const uint32_t g = j / (8 * tn), in = j - g * 8 * tn;
             const uint32_t rows = n - g * 8 < 8 ? n - g * 8 : 8;
             t->tn = __builtin_amdgcn_readfirstlane(in / rows);
-            t->row0 = t->lo + __builtin_amdgcn_readfirstlane((g * 8 + in % rows) * (uint32_t)bm);
+            t->row0 = __builtin_amdgcn_readfirstlane(lo + (int32_t)((g * 8 + in % rows) * (uint32_t)bm));
             return true;
         }
         before += __shfl(upto, 63);
@@ -125,7 +125,7 @@ __global__ __launch_bounds__(256) void grouped_narrow_kernel(GroupedArgs p) {
     __shared__ __attribute__((aligned(16))) uint16_t As[64 * PITCH], Bs[64 * PITCH];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     if (blockIdx.x == 0 && wave == 0) check_offsets(p);
-    int32_t lo, hi;
+    int32_t lo = 0, hi;
     int64_t m0, n0, m_end, k_len;
     int e;
     if constexpr (OP == GEMM_GROUPED_TN) {
@@ -141,9 +141,8 @@ __global__ __launch_bounds__(256) void grouped_narrow_kernel(GroupedArgs p) {
         RowTile t;
         if (!find_row_tile(p, 64, blockIdx.x, &t)) return;
         e = t.e;
-        lo = t.lo;
         m0 = t.row0;
-        m_end = t.hi;
+        m_end = t.end;
         n0 = (int64_t)t.tn * 64;
         k_len = p.K;
     }
@@ -248,13 +247,15 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_tile_kernel(GroupedArg
     if (blockIdx.x == 0 && threadIdx.x < 64) check_offsets(p);
     T tile;
     if constexpr (OP == GEMM_GROUPED_TN) {
-        // XCD x takes the x-th eighth of every expert's tiles, so the XCDs'
-        // shares are equal however uneven the groups are
-        const int tiles = p.tiles_m * p.tiles_n * p.parts, per = (tiles + 7) / 8;
-        const int j = blockIdx.x / 8, e = j / per;
-        const int u = (int)(blockIdx.x % 8) * per + (j - e * per);
-        if (u >= tiles) return;
-        const int t = u / p.parts, part = u - t * p.parts;
+        // Each XCD takes an eighth of every expert's tiles, so that the shares
+        // are equal however uneven the groups are, another one for the next
+        // expert, as eighths differ by a tile; part by part, so that few XCDs
+        // read the same rows.
+        const int of_part = p.tiles_m * p.tiles_n, tiles = of_part * p.parts, per = (tiles + 7) / 8;
+        const int j = blockIdx.x / 8, e = j / per, eighth = (int)(blockIdx.x + e) % 8;
+        const int u = (int)((int64_t)tiles * eighth / 8) + (j - e * per);
+        if (u >= (int)((int64_t)tiles * (eighth + 1) / 8)) return;
+        const int part = u / of_part, t = u - part * of_part;
         const int64_t m0 = (int64_t)(t / p.tiles_n) * BM, n0 = (int64_t)(t % p.tiles_n) * BN;
         int32_t lo, hi;
         group_rows(p, e, &lo, &hi);
@@ -277,30 +278,31 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_tile_kernel(GroupedArg
         const Operand a = {(const char *)(p.A + (int64_t)lo * p.lda + m0), p.lda * 2, m_left * 2};
         const Operand b = {(const char *)(p.B + (int64_t)lo * p.ldb + n0), p.ldb * 2, n_left * 2};
         tile.template run<2>(smem, a, b, hi - lo);
-        tile.template store<8>(smem, [&](int r, int c, const int (&v)[8]) {
+        tile.store(smem, [&](int r, int c, const int (&v)[8]) {
             if (r < m_left && c < n_left) store_run<true>(out, (int64_t)e * p.K + m0 + r, n0 + c, v);
         });
     } else {
         RowTile t;
         if (!find_row_tile(p, BM, blockIdx.x, &t)) return;
         const int64_t n0 = (int64_t)t.tn * BN;
-        const int32_t m_left = t.hi - t.row0 < BM ? t.hi - t.row0 : BM;
+        const int32_t m_left = t.end - t.row0 < BM ? t.end - t.row0 : BM;
         const int32_t n_left = (int32_t)(p.N - n0 < BN ? p.N - n0 : BN);
         tile.template run<2>(smem, row_operand(p, t, m_left), column_operand<OP>(p, t.e, n0, n_left), (int32_t)p.K);
-        tile.template store<8>(smem, [&](int r, int c, const int (&v)[8]) {
+        tile.store(smem, [&](int r, int c, const int (&v)[8]) {
             if (r < m_left && c < n_left) store_run<false>(p, (int64_t)t.row0 + r, n0 + c, v);
         });
     }
 }
 
-// Few rows per expert (NN, NT): MB * 32 rows and BN columns per workgroup.
-// Bound by streaming B, so the contraction is dealt out to the NW waves 64 at
-// a time and each wave streams its share through S stages of LDS of its own:
-// no wave waits for another until their sums meet, in the order of the waves.
-template <int OP, int MB, int BN, int NW, int S>
+// Few rows per expert (NN, NT): 32 rows and 64 columns per workgroup.  Bound by
+// streaming B, so the contraction is dealt out to the 4 waves 64 at a time and
+// each wave streams its share through 3 stages of LDS of its own: no wave waits
+// for another until their sums meet, in the order of the waves.  32 rows of one
+// expert, K = 4096, N = 3584: 16 us, 1.8 TB/s of B (a 128 x 128 tile 25 us).
+template <int OP>
 struct StreamTile {
-    static constexpr int BM = MB * 32, FN = BN / 32;
-    static constexpr int A_LOADS = MB * 4, B_LOADS = BN / 8, LOADS = A_LOADS + B_LOADS;   // of 1 KB
+    static constexpr int BM = 32, BN = 64, FN = BN / 32, NW = 4, S = 3;
+    static constexpr int A_LOADS = BM / 8, B_LOADS = BN / 8, LOADS = A_LOADS + B_LOADS;   // of 1 KB
     static constexpr int A_BYTES = A_LOADS * 1024, STAGE = LOADS * 1024;
     static constexpr int THREADS = NW * 64, LDS_BYTES = NW * S * STAGE;
     static constexpr bool COL = OP == GEMM_GROUPED_NN;
@@ -345,11 +347,9 @@ struct StreamTile {
         typedef __attribute__((address_space(3))) i32x4_t lds_i32x4;
         typedef __attribute__((address_space(3))) i16x4_t lds_i16x4;
         typedef __attribute__((address_space(3))) f32x4_t lds_f32x4;
-        f32x16_t acc[MB][FN];
+        f32x16_t acc[FN];
 #pragma unroll
-        for (int i = 0; i < MB; ++i)
-#pragma unroll
-            for (int j = 0; j < FN; ++j) acc[i][j] = f32x16_t{};
+        for (int j = 0; j < FN; ++j) acc[j] = f32x16_t{};
         const int grp = lane >> 4, te = (lane & 15) >> 2, tq = lane & 3;
 #pragma unroll
         for (int s = 0; s < S - 1; ++s)
@@ -361,12 +361,9 @@ struct StreamTile {
             lds_t *const at = own + st * STAGE, *const bt = at + A_BYTES;
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-                i32x4_t af[MB], bf[FN];
-#pragma unroll
-                for (int i = 0; i < MB; ++i) {
-                    const int r = i * 32 + (lane & 31);
-                    af[i] = *(lds_i32x4 *)(at + r * 128 + (((2 * ks + (lane >> 5)) ^ row_swz(r)) << 4));
-                }
+                i32x4_t bf[FN];
+                const int m = lane & 31;
+                const i32x4_t af = *(lds_i32x4 *)(at + m * 128 + (((2 * ks + (lane >> 5)) ^ row_swz(m)) << 4));
 #pragma unroll
                 for (int j = 0; j < FN; ++j) {
                     if constexpr (COL) {
@@ -382,23 +379,19 @@ struct StreamTile {
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < MB; ++i)
-#pragma unroll
-                    for (int j = 0; j < FN; ++j) acc[i][j] = mma(af[i], bf[j], acc[i][j]);
+                for (int j = 0; j < FN; ++j) acc[j] = mma(af, bf[j], acc[j]);
             }
             // the reads are done before the next issue overwrites their stage
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
             if (++st == S) st = 0;
         }
 #pragma unroll
-        for (int i = 0; i < MB; ++i)
+        for (int j = 0; j < FN; ++j)
 #pragma unroll
-            for (int j = 0; j < FN; ++j)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const f32x4_t v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-                    *(lds_f32x4 *)(own + ((i * 32 + (lane & 31)) * BN + j * 32 + 8 * q + 4 * (lane >> 5)) * 4) = v;
-                }
+            for (int q = 0; q < 4; ++q) {
+                const f32x4_t v = {acc[j][4 * q], acc[j][4 * q + 1], acc[j][4 * q + 2], acc[j][4 * q + 3]};
+                *(lds_f32x4 *)(own + ((lane & 31) * BN + j * 32 + 8 * q + 4 * (lane >> 5)) * 4) = v;
+            }
         __syncthreads();
         for (int u = tid; u < BM * BN / 8; u += THREADS) {
             const int r = u / (BN / 8), c = u % (BN / 8) * 8;
@@ -420,28 +413,28 @@ struct StreamTile {
     }
 };
 
-template <int OP, int MB, int BN, int NW, int S>
-__global__ __launch_bounds__(NW * 64) void grouped_stream_kernel(GroupedArgs p) {
-    using T = StreamTile<OP, MB, BN, NW, S>;
+template <int OP>
+__global__ __launch_bounds__(StreamTile<OP>::THREADS) void grouped_stream_kernel(GroupedArgs p) {
+    using T = StreamTile<OP>;
     extern __shared__ __attribute__((aligned(1024))) char smem_generic[];
     if (blockIdx.x == 0 && threadIdx.x < 64) check_offsets(p);
     RowTile t;
     if (!find_row_tile(p, T::BM, blockIdx.x, &t)) return;
-    const int64_t n0 = (int64_t)t.tn * BN;
-    const int32_t m_left = t.hi - t.row0 < T::BM ? t.hi - t.row0 : T::BM;
-    const int32_t n_left = (int32_t)(p.N - n0 < BN ? p.N - n0 : BN);
+    const int64_t n0 = (int64_t)t.tn * T::BN;
+    const int32_t m_left = t.end - t.row0 < T::BM ? t.end - t.row0 : T::BM;
+    const int32_t n_left = (int32_t)(p.N - n0 < T::BN ? p.N - n0 : T::BN);
     T::run((lds_t *)smem_generic, row_operand(p, t, m_left), column_operand<OP>(p, t.e, n0, n_left),
            (int32_t)p.K, [&](int r, int c, const int (&v)[8]) {
                if (r < m_left && c < n_left) store_run<false>(p, (int64_t)t.row0 + r, n0 + c, v);
            });
 }
 
-template <int OP, int MB, int BN, int NW, int S>
+template <int OP>
 hipError_t launch_stream(GroupedArgs &a, hipStream_t s) {
-    using T = StreamTile<OP, MB, BN, NW, S>;
-    a.tiles_n = (int32_t)((a.N + BN - 1) / BN);
+    using T = StreamTile<OP>;
+    a.tiles_n = (int32_t)((a.N + T::BN - 1) / T::BN);
     const int64_t blocks = (a.rows / T::BM + (a.E < a.rows ? a.E : a.rows)) * a.tiles_n;
-    return launch_lds<grouped_stream_kernel<OP, MB, BN, NW, S>>(blocks, T::THREADS, T::LDS_BYTES, s, a);
+    return launch_lds<grouped_stream_kernel<OP>>(blocks, T::THREADS, T::LDS_BYTES, s, a);
 }
 
 template <int OP, int BM, int BN, int WGM, int WGN, int SA, int SB>
@@ -461,6 +454,7 @@ __global__ __launch_bounds__(256) void grouped_join_kernel(GroupedArgs p) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
         const int64_t row = i / runs, n = i % runs * 8;
         float x[8] = {};
+#pragma unroll 4
         for (int s = 0; s < p.parts; ++s) {
             Raw<true> r;
             load8<true, true>(r, p.slots + ((int64_t)s * p.E * p.K + row) * p.N, (uint32_t)n, (uint32_t)p.N);
@@ -484,52 +478,65 @@ double row_tiles(const GroupedArgs &a, int bm) {
     return t > live ? t : live;
 }
 
-// NN and NT: the tile with the least time, rounds of 256 workgroups times the
-// steps of 64 times a step's time (us, measured; a round costs about as much
-// where it is not full), but not less than the operands take from memory.
-// Large tiles do the most work per byte, small ones fill the CUs; of equals the
-// larger, which reads B less often where an expert has more rows than the mean.
-// Measured, us for 256 x 256, 128 x 256, 128 x 128, 64 x 64 and 32 x 64 streams
-// (rows : N : K : E): 16384 : 3584 : 4096 : 8 440, 490, 587, -, -;
-// 8000 : 1792 : 4096 : 64 254, 225, 247, -, -; 512 : 3584 : 4096 : 8 104, 64, 50,
-// 79, 92; 128 : 1024 : 2048 : 1 -, -, 20, 11, 8.4; 32 : 3584 : 4096 : 1 -, -, 35,
-// 18, 16.
+// NN and NT: the tile with the least time, which is taken as rounds of 256
+// workgroups (a round costs about as much where it is not full) times the steps
+// of 64 times `step`, plus `fixed` (the first loads, the last stores, waiting
+// for the memory that all of them want at once), in us, but not less than the
+// operands take from memory.  step and fixed are fitted to the times of 170
+// calls of 1..16384 rows, sizes 256..4096, 1..64 experts, where the choice is 1%
+// slower than the best on average.  Large tiles do the most work per byte, small
+// ones fill the CUs; of equals the larger, which reads B less often where an
+// expert has more rows than the mean.  Measured, us for 256 x 256, 128 x 256,
+// 128 x 128 (deep loads, one workgroup per CU / two per CU), 64 x 128, 32 x 64
+// streams (rows : K : N : E): 16384 : 4096 : 3584 : 8 435, 500, 576 / 509, 679,
+// 1420; 8000 : 4096 : 1792 : 64 235, 224, 245 / 237, 266, 463; 10807 : 896 : 1408 :
+// 1 51, 40, 46 / 37, 46, 144; 512 : 4096 : 3584 : 8 75, 69, 50 / 53, 74, 88; 1160 :
+// 1088 : 960 : 6 26, 18, 12 / 13, 10, 18; 128 : 2048 : 1024 : 1 26, 27, 17 / 18, 13,
+// 8.4.
 template <int OP>
 hipError_t launch_rows(GroupedArgs &a, hipStream_t s) {
     struct Option {
         int bm, bn;
-        double step;
+        double step, fixed;
     };
-    const Option options[] = {{256, 256, 1.7}, {128, 256, 0.96}, {128, 128, 0.6}, {64, 64, 0.34}, {32, 64, 0.25}};
+    const Option options[] = {{256, 256, 1.76, 15.6}, {128, 256, 1.13, 8.0}, {128, 128, 0.71, 1.3},
+                              {64, 128, 0.47, 1.4}, {32, 64, 0.22, 1.4}};
     const double live = a.E < a.rows ? a.E : a.rows, steps = ceil_div((double)a.K, 64);
     const double floor_us = 2.0 * (live * a.K * a.N + (double)a.rows * (a.K + a.N)) / 5.0e6;
     int best = 0;
-    double best_us = 0;
+    double best_us = 0, best_rounds = 0;
     for (int i = 0; i < 5; ++i) {
         const Option &o = options[i];
-        double us = ceil_div(row_tiles(a, o.bm) * ceil_div((double)a.N, o.bn), kCus) * steps * o.step;
+        const double rounds = ceil_div(row_tiles(a, o.bm) * ceil_div((double)a.N, o.bn), kCus);
+        double us = rounds * (steps * o.step + o.fixed);
         if (us < floor_us) us = floor_us;
         if (i == 0 || us < 0.97 * best_us) {
             best = i;
             best_us = us;
+            best_rounds = rounds;
         }
     }
     switch (best) {
     case 0: return launch_tile<OP, 256, 256, 2, 4, 2, 3>(a, s);
     case 1: return launch_tile<OP, 128, 256, 2, 4, 3, 3>(a, s);
-    case 2:    // one round: deep loads, one workgroup per CU; more: two per CU
-        if (row_tiles(a, 128) * ceil_div((double)a.N, 128) > kCus) return launch_tile<OP, 128, 128, 2, 4, 2, 3>(a, s);
+    case 2:
+        if (best_rounds > 1) return launch_tile<OP, 128, 128, 2, 2, 2, 3>(a, s);
         return launch_tile<OP, 128, 128, 2, 4, 4, 4>(a, s);
-    case 3: return launch_stream<OP, 2, 64, 4, 2>(a, s);
-    default: return launch_stream<OP, 1, 64, 4, 3>(a, s);
+    case 3: return launch_tile<OP, 64, 128, 2, 2, 3, 3>(a, s);
+    default: return launch_stream<OP>(a, s);
     }
 }
 
 // TN: 256 x 256 tiles, or 128 x 128 with two workgroups per CU, so that one
 // stores while the other loads: better for short groups, whose time is the
 // stores (us for 256 / 128: 188 rows per expert 158 / 126, 2048 rows 431 / 556),
-// and where there are fewer large tiles than CUs.  With few of the small ones
-// too, `parts` workgroups share a tile's rows and a second kernel adds them.
+// and where there are fewer large tiles than CUs, unless those run in one round
+// and the small ones do not (118 rows, 3480 x 1240, 2 experts in 32 bits: 13 /
+// 18).  With few of the small ones too, `parts` workgroups share a tile's rows
+// and a second kernel adds them, as many as take the least time, from about 0.5
+// us per step of 64 rows, and for the second kernel 4 us and the parts' traffic
+// (16030 rows, 1296 x 304, 2 experts: 1 part 76 us, 4 39, 8 36, 16 41; 7984 rows,
+// 768 x 512, 8 experts: 1 part 20 us, 2 26).
 struct TnChoice {
     bool large;
     int parts;
@@ -537,25 +544,32 @@ struct TnChoice {
 TnChoice tn_choice(int64_t rows, int64_t K, int64_t N, int64_t E) {
     const int64_t large = E * ((K + 255) / 256) * ((N + 255) / 256);
     const int64_t small = E * ((K + 127) / 128) * ((N + 127) / 128);
-    const int64_t steps = rows / E / 64;
-    if (large >= kCus && rows / E >= 448) return {true, 1};
-    int64_t parts = 2 * kCus / small < steps / 4 ? 2 * kCus / small : steps / 4;
-    if (parts > 16) parts = 16;
-    return {false, (int)(parts < 2 ? 1 : parts)};
+    if (large >= kCus ? rows / E >= 448 : small > 2 * kCus) return {true, 1};
+    const double steps = (double)(rows / E) / 64, part_us = (double)E * K * N * 8 / 6.0e6;
+    int parts = 1;
+    double best_us = 0.5 * steps;
+    for (int p = 2; p <= 16 && p * small <= 2 * kCus; ++p) {
+        const double us = 0.5 * steps / p + 4 + p * part_us;
+        if (us < best_us) {
+            parts = p;
+            best_us = us;
+        }
+    }
+    return {false, parts};
 }
-hipError_t launch_tn(GroupedArgs &a, hipStream_t s) {
+hipError_t launch_tn(GroupedArgs &a, int max_parts, hipStream_t s) {
     const TnChoice c = tn_choice(a.rows, a.K, a.N, a.E);
     if (c.large) return launch_tile<GEMM_GROUPED_TN, 256, 256, 2, 4, 2, 2>(a, s);
-    a.parts = c.parts;
+    a.parts = c.parts < max_parts ? c.parts : max_parts;    // (the slots hold max_parts)
     hipError_t e = launch_tile<GEMM_GROUPED_TN, 128, 128, 2, 2, 2, 3>(a, s);
-    if (e != hipSuccess || c.parts == 1) return e;
+    if (e != hipSuccess || a.parts == 1) return e;
     const int64_t blocks = ((int64_t)a.E * a.K * (a.N / 8) + 255) / 256;
     hipLaunchKernelGGL(grouped_join_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
 template <int OP>
-hipError_t launch_op(GroupedArgs &a, bool wide, hipStream_t s) {
+hipError_t launch_op(GroupedArgs &a, bool wide, int max_parts, hipStream_t s) {
     if (!wide) {
         a.tiles_n = (int32_t)((a.N + 63) / 64);
         a.tiles_m = (int32_t)((a.K + 63) / 64);
@@ -564,15 +578,14 @@ hipError_t launch_op(GroupedArgs &a, bool wide, hipStream_t s) {
         hipLaunchKernelGGL(grouped_narrow_kernel<OP>, dim3((unsigned)(row_tiles * a.tiles_n)), dim3(256), 0, s, a);
         return hipGetLastError();
     }
-    if constexpr (OP == GEMM_GROUPED_TN) return launch_tn(a, s);
+    if constexpr (OP == GEMM_GROUPED_TN) return launch_tn(a, max_parts, s);
     else return launch_rows<OP>(a, s);
 }
 
-// Bytes of the parts of any call of a plan.
-int64_t slot_bytes(const gemm_grouped_desc_t &d) {
-    if (d.op != GEMM_GROUPED_TN || d.N % 8 != 0 || d.K % 8 != 0) return 0;
-    const int64_t parts = tn_choice(d.M, d.K, d.N, d.E).parts;   // most for the most rows
-    return parts > 1 ? parts * d.E * d.K * d.N * (int64_t)sizeof(float) : 0;
+// Parts of any call of a plan: most for the most rows.
+int most_parts(const gemm_grouped_desc_t &d) {
+    if (d.op != GEMM_GROUPED_TN || d.N % 8 != 0 || d.K % 8 != 0) return 1;
+    return tn_choice(d.M, d.K, d.N, d.E).parts;
 }
 
 int validate(const gemm_grouped_desc_t &d) {
@@ -602,7 +615,8 @@ struct gemm_grouped_plan_s {
     gemm_grouped_desc_t d;    // strides filled in
     int device;
     int32_t *err;
-    float *slots;        // parts of weight gradients (tn_choice), or null
+    int parts;           // most parts of a weight gradient
+    float *slots;        // room for them, or null
     int64_t slot_bytes;
 };
 
@@ -621,7 +635,8 @@ int gemm_grouped_plan(const gemm_grouped_desc_t *desc, gemm_grouped_plan_t *out)
     if (!p->d.ldc) p->d.ldc = p->d.N;
     hipError_t e = hipGetDevice(&p->device);
     if (e == hipSuccess) e = hipMalloc((void **)&p->err, 16);
-    p->slot_bytes = slot_bytes(p->d);
+    p->parts = most_parts(p->d);
+    p->slot_bytes = p->parts > 1 ? p->parts * p->d.E * p->d.K * p->d.N * (int64_t)sizeof(float) : 0;
     if (e == hipSuccess && p->slot_bytes) e = hipMalloc((void **)&p->slots, p->slot_bytes);
     // a blocking copy: the word is zero before any later launch on any stream
     const int32_t zero[4] = {0, 0, 0, 0};
@@ -666,9 +681,9 @@ int gemm_grouped_run(gemm_grouped_plan_t p, const void *A, const void *B, const 
     const int64_t c_elems = d.out_dtype == GEMM_RS_F32 ? 4 : 8;
     const bool wide = d.N % 8 == 0 && d.K % 8 == 0 && d.lda % 8 == 0 && d.ldb % 8 == 0 &&
                       d.ldc % c_elems == 0 && aligned(A, 16) && aligned(B, 16) && aligned(C, 16);
-    const hipError_t e = d.op == GEMM_GROUPED_NN   ? launch_op<GEMM_GROUPED_NN>(a, wide, s)
-                         : d.op == GEMM_GROUPED_NT ? launch_op<GEMM_GROUPED_NT>(a, wide, s)
-                                                   : launch_op<GEMM_GROUPED_TN>(a, wide, s);
+    const hipError_t e = d.op == GEMM_GROUPED_NN   ? launch_op<GEMM_GROUPED_NN>(a, wide, p->parts, s)
+                         : d.op == GEMM_GROUPED_NT ? launch_op<GEMM_GROUPED_NT>(a, wide, p->parts, s)
+                                                   : launch_op<GEMM_GROUPED_TN>(a, wide, p->parts, s);
     return e == hipSuccess ? GEMM_RS_OK : GEMM_RS_ERR_HIP;
 }
 

@@ -48,37 +48,32 @@ __global__ __launch_bounds__(64 * WGM * WGN) void q8_tile_kernel(Q8Args p) {
     const Operand a = {(const char *)p.a + m0 * p.lda, p.lda, m_left};
     const Operand w = {(const char *)p.w + n0 * p.ldw, p.ldw, n_left};
     tile.template run<1>(smem, a, w, (int32_t)p.K);
-    if (p.wide_out && n_left % 8 == 0) {
-        // a lane's 8 columns are the same in every row it stores
-        const int c0 = (int)(threadIdx.x % (BN / 8)) * 8;
-        float sw[8], bias[8];
+    // a lane's 8 columns are the same in every row it stores
+    const int c0 = (int)(threadIdx.x % (BN / 8)) * 8;
+    float sw[8], bias[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int64_t n = n0 + (c0 < n_left ? c0 : 0) + e;
-            sw[e] = p.w_scale[n];
-            bias[e] = p.bias ? p.bias[n] : 0.0f;
-        }
-        tile.template store<8>(smem, [&](int r, int c, const int (&v)[8]) {
-            if (r >= m_left || c >= n_left) return;
-            const int64_t m = m0 + r;
-            const float sa = p.a_scale[m];
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = scaled(v[e], sa, sw[e], p.bias ? &bias[e] : nullptr);
-            const uint32_t at = (uint32_t)(n0 + c), cols = (uint32_t)p.N;
-            if (p.out_f32) store8<true, true>(row_of(p.D, m, p.ldd, 4), at, cols, x);
-            else store8<false, true>(row_of(p.D, m, p.ldd, 2), at, cols, x);
-        });
-    } else {
-        const int c1 = (int)threadIdx.x % BN;
-        const int64_t n = n0 + (c1 < n_left ? c1 : 0);
-        const float sw = p.w_scale[n], bias = p.bias ? p.bias[n] : 0.0f;
-        tile.template store<1>(smem, [&](int r, int c, const int (&v)[1]) {
-            if (r >= m_left || c >= n_left) return;
-            const int64_t m = m0 + r;
-            store_one(p, m, n, scaled(v[0], p.a_scale[m], sw, p.bias ? &bias : nullptr));
-        });
+    for (int e = 0; e < 8; ++e) {
+        const int64_t n = n0 + c0 + e < p.N ? n0 + c0 + e : p.N - 1;
+        sw[e] = p.w_scale[n];
+        bias[e] = p.bias ? p.bias[n] : 0.0f;
     }
+    tile.store(smem, [&](int r, int c, const int (&v)[8]) {
+        if (r >= m_left || c >= n_left) return;
+        const int64_t m = m0 + r;
+        const float sa = p.a_scale[m];
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = scaled(v[e], sa, sw[e], p.bias ? &bias[e] : nullptr);
+        const uint32_t at = (uint32_t)(n0 + c), cols = (uint32_t)p.N;
+        void *const to = row_of(p.D, m, p.ldd, p.out_f32 ? 4 : 2);
+        if (p.wide_out) {
+            if (p.out_f32) store8<true, true>(to, at, cols, x);
+            else store8<false, true>(to, at, cols, x);
+        } else {
+            if (p.out_f32) store8<true, false>(to, at, cols, x);
+            else store8<false, false>(to, at, cols, x);
+        }
+    });
 }
 
 // Few rows: NB * 16 channels and up to MB * 16 rows per workgroup.  The
@@ -362,7 +357,7 @@ int gemm_q8_run(gemm_q8_plan_t p, const void *a, const void *a_scale, const void
     q.bias = (const float *)bias;
     q.D = D;
     q.out_f32 = d.out_dtype == GEMM_RS_F32;
-    q.wide_out = d.ldd % 8 == 0 && aligned(D, 16);
+    q.wide_out = d.N % 8 == 0 && d.ldd % 8 == 0 && aligned(D, 16);
     return launch_product(q, (hipStream_t)stream) == hipSuccess ? GEMM_RS_OK : GEMM_RS_ERR_HIP;
 }
 

@@ -136,9 +136,8 @@ struct Tile {
     static constexpr int LDS_BYTES = SA * A_BYTES + SB * B_BYTES;
     static_assert(SA >= 2 && (SB == SA || SB == SA + 1), "rings of A and B stages");
     // Loads of 1 KB per stage and operand, dealt out to all waves.
-    static constexpr int DW = NW;
-    static constexpr int AI = A_BYTES / 1024 / DW, BI = B_BYTES / 1024 / DW;
-    static_assert(AI * DW * 1024 == A_BYTES && BI * DW * 1024 == B_BYTES, "whole loads per wave");
+    static constexpr int AI = A_BYTES / 1024 / NW, BI = B_BYTES / 1024 / NW;
+    static_assert(AI * NW * 1024 == A_BYTES && BI * NW * 1024 == B_BYTES, "whole loads per wave");
     static_assert(WM % 32 == 0 && WN % 32 == 0, "whole blocks per wave");
     static_assert(!A_COL || BM >= 128, "column swizzle needs 16 chunks per row");
     static_assert(!B_COL || BN >= 128, "column swizzle needs 16 chunks per row");
@@ -152,11 +151,11 @@ struct Tile {
 
     ACC acc[FM][FN];
 
-    // Load i of wave w covers 1 KB of an operand's tile, at (i * DW + w) * 1024:
+    // Load i of wave w covers 1 KB of an operand's tile, at (i * NW + w) * 1024:
     // this lane's chunk of it, and its offset from the window's base.
     template <bool COL, int B>
     static __device__ __forceinline__ int load_row(int i, int w, int lane) {
-        return COL ? (i * DW + w) * (64 / (B / 8)) + lane / (B / 8) : (i * DW + w) * 8 + lane / 8;
+        return COL ? (i * NW + w) * (64 / (B / 8)) + lane / (B / 8) : (i * NW + w) * 8 + lane / 8;
     }
     template <bool COL, int B>
     static __device__ __forceinline__ int load_chunk(int i, int w, int lane) {
@@ -229,9 +228,9 @@ struct Tile {
             const int j = isa ? i : i - AI;
             uint32_t v = voff[i];
             if (isa ? !A_COL : !B_COL)
-                v = (isa ? a_chunk : b_chunk)[DW == 8 ? 0 : j & 1] < (isa ? l.a_chunks : l.b_chunks) ? v : 0xfffffff0u;
+                v = (isa ? a_chunk : b_chunk)[NW == 8 ? 0 : j & 1] < (isa ? l.a_chunks : l.b_chunks) ? v : 0xfffffff0u;
             load_to_lds(isa ? l.a : l.b, v,
-                        smem_base + (isa ? l.a_to * A_BYTES : B_AT + l.b_to * B_BYTES) + (j * DW + wave) * 1024);
+                        smem_base + (isa ? l.a_to * A_BYTES : B_AT + l.b_to * B_BYTES) + (j * NW + wave) * 1024);
         };
 
         // LDS addresses of this lane's fragments: few registers, and constants
@@ -394,15 +393,13 @@ struct Tile {
         }
     }
 
-    // Hands the tile out as f(row, column, v[RUN]) for runs of RUN columns (8,
-    // or 1 where the output's rows are not aligned), each run once, whole rows
-    // by neighbouring lanes.  Accumulators pass through LDS one 32-row block
+    // Hands the tile out as f(row, column, v[8]) for runs of 8 columns, each run
+    // once, whole rows by neighbouring lanes.  Accumulators pass through LDS one 32-row block
     // row of every wave at a time: the direct layout would store 8 bytes per
     // row and instruction.  16-byte chunk c of a staged row r sits at
     // c ^ (r % 16).
-    template <int RUN, class F>
+    template <class F>
     __device__ __forceinline__ void store(lds_t *smem, F f) const {
-        static_assert(RUN == 8 || RUN == 1, "");
         constexpr int SROWS = WGM * 32, ROW = BN * 4, SBYTES = SROWS * ROW;
         constexpr bool TWICE = 2 * SBYTES <= LDS_BYTES;   // alternate between two halves
         static_assert(SBYTES <= LDS_BYTES, "a stripe fits");
@@ -410,7 +407,6 @@ struct Tile {
         const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         const int wm = wave / WGN, wn = wave % WGN;
         typedef __attribute__((address_space(3))) i32x4_t lds_i32x4;
-        typedef __attribute__((address_space(3))) int32_t lds_i32;
         wait_loads<0>();                                  // the empty loads past the last step
         lds_only_barrier();                               // every wave is done with the stages
 #pragma unroll
@@ -434,26 +430,14 @@ struct Tile {
                     }
             }
             lds_only_barrier();
-            if constexpr (RUN == 8) {
-                constexpr int LPR = BN / 8;
+            constexpr int LPR = BN / 8;
 #pragma unroll
-                for (int u = 0; u < SROWS * LPR; u += THREADS) {
-                    const int rr = (u + tid) / LPR, c = (tid % LPR) * 2;
-                    const i32x4_t lo = *(lds_i32x4 *)(s + rr * ROW + ((c ^ (rr & 15)) << 4));
-                    const i32x4_t hi = *(lds_i32x4 *)(s + rr * ROW + (((c + 1) ^ (rr & 15)) << 4));
-                    const int v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                    f((rr >> 5) * WM + i * 32 + (rr & 31), (tid % LPR) * 8, v);
-                }
-            } else {
-                // a thread's columns are all tid % BN
-                static_assert(THREADS % BN == 0, "whole rows per turn");
-                const int c = tid % BN;
-#pragma unroll 8
-                for (int u = 0; u < SROWS; u += THREADS / BN) {
-                    const int rr = u + tid / BN;
-                    const int v[1] = {*(lds_i32 *)(s + rr * ROW + (((c >> 2) ^ (rr & 15)) << 4) + (c & 3) * 4)};
-                    f((rr >> 5) * WM + i * 32 + (rr & 31), c, v);
-                }
+            for (int u = 0; u < SROWS * LPR; u += THREADS) {
+                const int rr = (u + tid) / LPR, c = (tid % LPR) * 2;
+                const i32x4_t lo = *(lds_i32x4 *)(s + rr * ROW + ((c ^ (rr & 15)) << 4));
+                const i32x4_t hi = *(lds_i32x4 *)(s + rr * ROW + (((c + 1) ^ (rr & 15)) << 4));
+                const int v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                f((rr >> 5) * WM + i * 32 + (rr & 31), (tid % LPR) * 8, v);
             }
         }
     }
