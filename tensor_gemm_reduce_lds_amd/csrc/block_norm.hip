@@ -7,12 +7,12 @@
 // 8000 x 8192, f32 stream: 148 us, 5.3 TB/s (a large copy on the same card runs
 // at 4.95 TB/s).
 //
-// Backward: a workgroup walks a run of consecutive rows, loading one row while
-// it works on the one before, and keeps the sums for dw_post, dw_pre and
+// Backward: a workgroup walks a run of consecutive rows (loading one row while
+// it works on the one before, where that helps) and keeps the sums for dw_post, dw_pre and
 // dgate of its columns in registers; two joins per row (mean squares of x' and
 // y and the product a.x' together, then b.y).  The partial sums go to the
 // workspace once per workgroup and a second kernel adds them in a fixed order.
-// 8192 x 8192 bf16: 180 us, 4.5 TB/s; 1000 x 4096, f32 stream: 25 us (few rows
+// 8192 x 8192 bf16: 165 us, 4.9 TB/s; 1000 x 4096, f32 stream: 23 us (few rows
 // per workgroup, and the partial sums are a third of the traffic).
 #include <math.h>
 #include <stdlib.h>
@@ -43,21 +43,40 @@ struct NormArgs {
     float *part;
 };
 
-// Columns c..c+7 of a row of parameters.
-template <bool WIDE>
-__device__ __forceinline__ void load_param(const NormArgs &a, const void *row, uint32_t c, float add, float *out) {
-    const uint32_t cols = (uint32_t)a.cols;
-    if (a.param_f32) {
-        Raw<true> r;
-        load8<true, WIDE>(r, row, c, cols);
+// This thread's columns of up to three rows of parameters (null: left as they
+// are), in[i] + add[i] to out[i]; all loads before the first use of one.
+template <bool WIDE, int EPT, int THREADS, int N, bool F32>
+__device__ __forceinline__ void load_params_of(uint32_t cols, const void *const (&in)[N], const float (&add)[N],
+                                               float (*const (&out)[N])[EPT]) {
+    Raw<F32> r[N][EPT / 8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) out[e] = raw_at(r, e) + add;
-    } else {
-        Raw<false> r;
-        load8<false, WIDE>(r, row, c, cols);
+    for (int i = 0; i < N; ++i)
+        if (in[i])
 #pragma unroll
-        for (int e = 0; e < 8; ++e) out[e] = raw_at(r, e) + add;
-    }
+            for (int k = 0; k < EPT / 8; ++k) {
+                const uint32_t c = (uint32_t)(k * THREADS + threadIdx.x) * 8;
+                r[i][k] = Raw<F32>{};
+                if (c < cols) load8<F32, WIDE>(r[i][k], in[i], c, cols);
+            }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (in[i])
+#pragma unroll
+            for (int j = 0; j < EPT; ++j) (*out[i])[j] = raw_at(r[i][j / 8], j % 8) + add[i];
+}
+template <bool WIDE, int EPT, int THREADS, int N>
+__device__ __forceinline__ void load_params(const NormArgs &a, const void *const (&in)[N], const float (&add)[N],
+                                            float (*const (&out)[N])[EPT]) {
+    if (a.param_f32) load_params_of<WIDE, EPT, THREADS, N, true>((uint32_t)a.cols, in, add, out);
+    else load_params_of<WIDE, EPT, THREADS, N, false>((uint32_t)a.cols, in, add, out);
+}
+
+// The gate row of a row, and a row of the gate.
+__device__ __forceinline__ int64_t gate_of(const NormArgs &a, int64_t row) {
+    return (uint32_t)row / (uint32_t)a.rows_per_gate;
+}
+__device__ __forceinline__ const void *gate_at(const NormArgs &a, int64_t gate_row) {
+    return row_of(a.gate, gate_row, a.cols, a.param_f32 ? 4 : 2);
 }
 
 // THREADS threads hold a row of up to THREADS * EPT columns: thread t has
@@ -73,17 +92,9 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
 
     float w_post[EPT], w_pre[EPT], gate[EPT];
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-        const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
-        float *wo = w_post + k * 8, *wp = w_pre + k * 8, *g = gate + k * 8;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) wo[e] = wp[e] = g[e] = 1.0f;
-        if (c < cols) {
-            if (a.post) load_param<WIDE>(a, a.w_post, c, a.weight_offset, wo);
-            if (a.pre) load_param<WIDE>(a, a.w_pre, c, a.weight_offset, wp);
-        }
-    }
-    int64_t gate_row = -1;
+    for (int i = 0; i < EPT; ++i) w_post[i] = w_pre[i] = gate[i] = 1.0f;
+    load_params<WIDE, EPT, THREADS, 2>(a, {a.w_post, a.w_pre}, {a.weight_offset, a.weight_offset}, {&w_post, &w_pre});
+    int64_t gate_end = 0;
     for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
         Raw<SF> xr[VPT];
         Raw<YF> yr[VPT];
@@ -98,13 +109,10 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
                 if (a.has_y) load8<YF, WIDE>(yr[k], row_of(a.y, row, a.ld_y, YF ? 4 : 2), c, cols);
             }
         }
-        if (a.gated && row / a.rows_per_gate != gate_row) {
-            gate_row = row / a.rows_per_gate;
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
-                if (c < cols) load_param<WIDE>(a, row_of(a.gate, gate_row, a.cols, a.param_f32 ? 4 : 2), c, 0.0f, gate + k * 8);
-            }
+        if (a.gated && row >= gate_end) {
+            const int64_t g = gate_of(a, row);
+            gate_end = (g + 1) * a.rows_per_gate;
+            load_params<WIDE, EPT, THREADS, 1>(a, {gate_at(a, g)}, {0.0f}, {&gate});
         }
 #pragma unroll
         for (int k = 0; k < VPT; ++k)
@@ -187,7 +195,7 @@ struct Own<EPT, THREADS, true> {
     __device__ __forceinline__ void set(int i, float x) { at[i / 4 * THREADS][i % 4] = x; }
 };
 // Rows of more than 8192 columns keep w_pre and the sums for dw_post in LDS
-// (8192 x 16384 bf16: 1449 us with all in registers and spills, 471).
+// (8192 x 16384 bf16: 1449 us with all in registers and spills, 390).
 template <int EPT, int THREADS>
 constexpr bool kOwnInLds = EPT * THREADS > 8192;
 
@@ -220,23 +228,6 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
     w_pre.place(own);
     s_post.place(own + w_pre.BYTES);
     float gw[EPT], s_dy[EPT], s_pre[EPT];
-#pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-        const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
-        float *wo = gw + k * 8, wp[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            wo[e] = wp[e] = 1.0f;
-            s_dy[k * 8 + e] = s_pre[k * 8 + e] = 0.0f;
-            s_post.set(k * 8 + e, 0.0f);
-        }
-        if (c < cols) {
-            if (a.post) load_param<WIDE>(a, a.w_post, c, a.weight_offset, wo);
-            if (a.pre) load_param<WIDE>(a, a.w_pre, c, a.weight_offset, wp);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w_pre.set(k * 8 + e, wp[e]);
-    }
     auto take = [&](Row &r, int64_t row) __attribute__((always_inline)) {
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
@@ -253,7 +244,24 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
             }
         }
     };
-    int64_t gate_row = -1, gate_end = first;
+    // A row of the gate and w_post + offset (1 where there is none).
+    auto load_gate = [&](int64_t row, float (&g)[EPT], float (&w)[EPT]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) g[i] = w[i] = 1.0f;
+        load_params<WIDE, EPT, THREADS, 2>(a, {a.gated ? gate_at(a, row) : nullptr, a.w_post}, {0.0f, a.weight_offset},
+                                           {&g, &w});
+    };
+    int64_t gate_row = 0, gate_end = 0;
+    auto begin_gate = [&](int64_t row) __attribute__((always_inline)) {
+        if (a.gated) {
+            gate_row = gate_of(a, row);
+            gate_end = (gate_row + 1) * a.rows_per_gate;
+        }
+        float g[EPT], w[EPT];
+        load_gate(gate_row, g, w);
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) gw[i] = g[i] * w[i];
+    };
     // Ends a gate row's rows: its part of dw_post, and its dgate, whole if all
     // its rows are this workgroup's, else a part: the head slot for the gate
     // row of the first row, the tail slot for a later one.
@@ -263,46 +271,41 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
         if (hi > a.rows) hi = a.rows;
         const bool whole = lo >= first && hi <= last;
         float *to = whole ? a.dgate + gate_row * a.cols
-                          : a.part + ((int64_t)blockIdx.x * 4 + (gate_row == first / a.rows_per_gate ? 2 : 3)) * a.cols;
+                          : a.part + ((int64_t)blockIdx.x * 4 + (gate_row == gate_of(a, first) ? 2 : 3)) * a.cols;
+        float g[EPT], w[EPT];
+        load_gate(gate_row, g, w);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
             const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
             if (c >= cols) continue;
-            float g[8], w[8];
-            load_param<WIDE>(a, row_of(a.gate, gate_row, a.cols, a.param_f32 ? 4 : 2), c, 0.0f, g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = 1.0f;
-            if (a.post) load_param<WIDE>(a, a.w_post, c, a.weight_offset, w);
+            float d[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 float &s = s_dy[k * 8 + e];
-                s_post.set(k * 8 + e, s_post.get(k * 8 + e) + g[e] * s);
-                w[e] *= s;
+                s_post.set(k * 8 + e, s_post.get(k * 8 + e) + g[k * 8 + e] * s);
+                d[e] = w[k * 8 + e] * s;
                 s = 0.0f;
             }
-            store8<true, WIDE>(to, c, cols, w);
+            store8<true, WIDE>(to, c, cols, d);
         }
     };
-    auto begin_gate = [&](int64_t row) __attribute__((always_inline)) {
-        gate_row = row / a.rows_per_gate;
-        gate_end = (gate_row + 1) * a.rows_per_gate;
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
-            if (c >= cols) continue;
-            float g[8];
-            float *w = gw + k * 8;
-            load_param<WIDE>(a, row_of(a.gate, gate_row, a.cols, a.param_f32 ? 4 : 2), c, 0.0f, g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] = 1.0f;
-            if (a.post) load_param<WIDE>(a, a.w_post, c, a.weight_offset, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[e] *= g[e];
-        }
-    };
-
+    // the first row's loads before the parameters': with few rows their latency
+    // is most of the time
     Row next;
     if constexpr (AHEAD) take(next, first);
+    {
+        float w[EPT];
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) {
+            s_dy[i] = s_pre[i] = 0.0f;
+            s_post.set(i, 0.0f);
+            w[i] = 1.0f;
+        }
+        load_params<WIDE, EPT, THREADS, 1>(a, {a.w_pre}, {a.weight_offset}, {&w});
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) w_pre.set(i, w[i]);
+        begin_gate(first);
+    }
     for (int64_t row = first; row < last; ++row) {
         Row r;
         if constexpr (AHEAD) {
@@ -311,8 +314,8 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
         } else {
             take(r, row);
         }
-        if (a.gated && row >= gate_end) {     // the first row, and each gate row's first
-            if (gate_row >= 0) end_gate();
+        if (a.gated && row >= gate_end) {
+            end_gate();
             begin_gate(row);
         }
         float s[3] = {0.0f, 0.0f, 0.0f};
@@ -368,7 +371,7 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
         }
     }
     if (a.gated) {
-        if (gate_row >= 0) end_gate();
+        end_gate();
     } else {
 #pragma unroll
         for (int i = 0; i < EPT; ++i) s_post.set(i, s_dy[i]);
@@ -459,7 +462,11 @@ void launch_forward(const NormArgs &a, bool sf, bool yf, bool quant, int64_t gri
 
 template <bool WIDE, int EPT, int THREADS>
 hipError_t launch_backward(const NormArgs &a, bool sf, bool yf, int64_t grid, hipStream_t s) {
-    constexpr bool AHEAD = !kOwnInLds<EPT, THREADS>;    // no registers for it there
+    // The next row is loaded ahead where its rows are aligned and registers are
+    // left for it (8192 x 8192 bf16: 122 us, 137 without; 4096 columns 67, 87).
+    // Unaligned rows end in a branch that the loads would wait at (8192 x 513:
+    // 32 us, 35 with the next row ahead).
+    constexpr bool AHEAD = WIDE && !kOwnInLds<EPT, THREADS>;
     constexpr int lds = 2 * Own<EPT, THREADS, kOwnInLds<EPT, THREADS>>::BYTES;
     if (sf && yf) return launch_lds<norm_backward_kernel<WIDE, EPT, THREADS, true, true, AHEAD>>(grid, THREADS, lds, s, a);
     if (sf) return launch_lds<norm_backward_kernel<WIDE, EPT, THREADS, true, false, AHEAD>>(grid, THREADS, lds, s, a);
