@@ -50,9 +50,10 @@ extern "C" {
  *               B (NN, NT) or C (TN) lies K (or N) rows of the stride
  *               after the one before.
  *   pad         must be 0
- * Any sizes and element-aligned addresses are accepted; sizes, strides and
- * addresses that are all multiples of 8 elements (16 bytes) take the
- * matrix-pipe kernels with direct loads to shared memory.
+ * Any sizes and element-aligned addresses are accepted.  Sizes, strides and
+ * addresses that are all multiples of 8 elements (16 bytes) take the kernels
+ * with direct loads to shared memory, others a kernel that loads element by
+ * element and is many times slower.
  */
 typedef struct gemm_grouped_desc {
     int64_t M, N, K;
@@ -84,6 +85,7 @@ GEMM_RS_API int gemm_grouped_plan(const gemm_grouped_desc_t *desc, gemm_grouped_
  *   offsets  int32 [E+1] on the device, non-decreasing, within 0..rows.
  *            Other values are clipped to that (no access leaves the
  *            arrays) and reported by gemm_grouped_status.
+ *   C        may not overlap an input
  * One plan of TN must not run on two streams at once (its workspace).
  * Returns OK, INVALID_ARG (NULL or misaligned pointers, rows out of range,
  * another device) or HIP.

@@ -14,8 +14,9 @@
  * gemm_q8_quantize makes a and a_scale from bfloat16 or float rows:
  *     a_scale[m] = max_k |x[m][k]| / 127
  *     a[m][k]    = round_to_nearest_even(x[m][k] * (127 * (1 / max_k |x[m][k]|)))
- * each step in 32-bit floats, rounded to nearest.  A row of zeros gets scale 0 and zeros; a row with a NaN or an infinity
- * gets scale NaN and zeros, so its products are NaN.
+ * each step in 32-bit floats, rounded to nearest.  A row of zeros gets scale
+ * 0 and zeros; a row with a NaN or an infinity gets scale NaN and zeros, so
+ * its products are NaN.
  *
  * Status codes and gemm_rs_strerror are those of gemm_rs.h.  All functions
  * are plain C, never throw, abort or print.
@@ -70,7 +71,8 @@ GEMM_RS_API int gemm_q8_plan(const gemm_q8_desc_t *desc, gemm_q8_plan_t *out);
  *   a       int8 [rows][lda], 16-byte aligned;   a_scale float [rows]
  *   w       int8 [N][ldw], 16-byte aligned;      w_scale float [N]
  *   bias    float [N], NULL without has_bias
- *   D       [rows][ldd] of out_dtype, element-aligned
+ *   D       [rows][ldd] of out_dtype, element-aligned; it may not overlap
+ *           an input
  * Returns OK, INVALID_ARG (missing, superfluous or misaligned pointers, rows
  * out of range, another device) or HIP.
  */
@@ -82,7 +84,7 @@ GEMM_RS_API int gemm_q8_run(gemm_q8_plan_t plan, const void *a, const void *a_sc
  * gemm_q8_quantize: rows x cols of `dtype` (row stride ldx elements) to int8
  * rows of stride ldq bytes and one float scale per row; columns
  * cols..ceil(cols/16)*16 of the output are zeros (ldq holds them).  Enqueued
- * on `stream`.  rows may be 0.  Returns OK, INVALID_ARG (NULL or misaligned
+ * on `stream`.  rows may be 0; q and scale may not overlap x.  Returns OK, INVALID_ARG (NULL or misaligned
  * pointers: x to its element; rows < 0, cols < 1, ldx < cols, ldq below
  * ceil(cols/16)*16, unknown type), UNSUPPORTED (cols of 2^17 or more, rows
  * or strides of 2^31 or more) or HIP.

@@ -8,10 +8,11 @@
 // at 4.95 TB/s).
 //
 // Backward: a workgroup walks a run of consecutive rows (loading one row while
-// it works on the one before, where that helps) and keeps the sums for dw_post, dw_pre and
-// dgate of its columns in registers; two joins per row (mean squares of x' and
-// y and the product a.x' together, then b.y).  The partial sums go to the
-// workspace once per workgroup and a second kernel adds them in a fixed order.
+// it works on the one before, where that helps) and keeps the sums for dw_post,
+// dw_pre and dgate of its columns in registers; two joins per row (mean squares
+// of x' and y and the product a.x' together, then b.y).  The partial sums go to
+// the workspace once per workgroup and a second kernel adds them in a fixed
+// order (6 to 7 us).
 // 8192 x 8192 bf16: 165 us, 4.9 TB/s; 1000 x 4096, f32 stream: 23 us (few rows
 // per workgroup, and the partial sums are a third of the traffic).
 #include <math.h>

@@ -6,8 +6,7 @@
 // int8), or the 64 rows of a column operand (bfloat16, stored with the
 // output axis contiguous).  Operands go from memory straight into rings of
 // SA and SB stages in LDS, 16 bytes per lane; loads run SA - 1 and SB - 1 steps
-// ahead.
-// Both kinds of LDS tile are XOR-swizzled in 16-byte chunks (by choosing the
+// ahead.  Both kinds of LDS tile are XOR-swizzled in 16-byte chunks (by choosing the
 // chunk that each lane fetches), so that fragment reads spread over the
 // banks; a column operand's fragments come from transposing LDS reads.
 //
@@ -15,8 +14,18 @@
 // descriptor that ends with the operand's last valid byte of the step, and
 // chunks past the end of the contraction are sent past the descriptor.  So no
 // value in a gap or past an end, NaN or not, enters a sum, and rows and
-// columns past the output are computed on repeated or zero values and never
-// stored.
+// columns past the output are computed on zeros or on other tiles' values and
+// never stored.
+//
+// Bounds.  A wave's WM x WN share of the output reads (WM + WN) * 128 bytes of
+// LDS for WM * WN / 256 cycles of the matrix pipe in a step, so small shares
+// are bound by LDS (128 x 128 tiles: 0.5 us a step, two thirds of it LDS reads
+// and loads into LDS at 128 bytes a cycle), 128 x 64 ones (256 x 256 tiles) by
+// the matrix pipe and, with every CU busy, by the board's power limit, which
+// takes the clock to about 1.6 GHz: 8192 x 8192 x 3584 in int8 2040 TOP/s,
+// 16384 rows over 8 experts of 4096 x 3584 in bfloat16 1100 TFLOP/s.  Reads and
+// loads one by one behind the matrix operations instead of in batches: 1024 x
+// 3584 x 8192 in int8 49 -> 39 us, 16384 rows 453 -> 438 us.
 #pragma once
 
 #include <type_traits>
