@@ -52,8 +52,8 @@ extern "C" {
  *   pad         must be 0
  * Any sizes and element-aligned addresses are accepted.  Sizes, strides and
  * addresses that are all multiples of 8 elements (16 bytes) take the kernels
- * with direct loads to shared memory, others a kernel that loads element by
- * element and is many times slower.
+ * with direct loads to shared memory, others a kernel that takes about twice as
+ * long (8000 rows, 64 experts of 4095 x 1791: 500 us, of 4096 x 1792: 220).
  */
 typedef struct gemm_grouped_desc {
     int64_t M, N, K;

@@ -57,13 +57,17 @@ __device__ __forceinline__ void load_params_of(uint32_t cols, const void *const 
             for (int k = 0; k < EPT / 8; ++k) {
                 const uint32_t c = (uint32_t)(k * THREADS + threadIdx.x) * 8;
                 r[i][k] = Raw<F32>{};
-                if (c < cols) load8<F32, WIDE>(r[i][k], in[i], c, cols);
+                if (c < cols) fetch8<F32, WIDE>(r[i][k], in[i], c, cols);
             }
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        if (in[i])
+        if (in[i]) {
+#pragma unroll
+            for (int k = 0; k < EPT / 8; ++k)
+                settle8<F32, WIDE>(r[i][k], (uint32_t)(k * THREADS + threadIdx.x) * 8, cols);
 #pragma unroll
             for (int j = 0; j < EPT; ++j) (*out[i])[j] = raw_at(r[i][j / 8], j % 8) + add[i];
+        }
 }
 template <bool WIDE, int EPT, int THREADS, int N>
 __device__ __forceinline__ void load_params(const NormArgs &a, const void *const (&in)[N], const float (&add)[N],
@@ -106,8 +110,8 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
             xr[k] = Raw<SF>{};
             yr[k] = Raw<YF>{};
             if (c < cols) {
-                load8<SF, WIDE>(xr[k], row_of(a.x, row, a.ld_x, SF ? 4 : 2), c, cols);
-                if (a.has_y) load8<YF, WIDE>(yr[k], row_of(a.y, row, a.ld_y, YF ? 4 : 2), c, cols);
+                fetch8<SF, WIDE>(xr[k], row_of(a.x, row, a.ld_x, SF ? 4 : 2), c, cols);
+                if (a.has_y) fetch8<YF, WIDE>(yr[k], row_of(a.y, row, a.ld_y, YF ? 4 : 2), c, cols);
             }
         }
         if (a.gated && row >= gate_end) {
@@ -116,12 +120,16 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
             load_params<WIDE, EPT, THREADS, 1>(a, {gate_at(a, g)}, {0.0f}, {&gate});
         }
 #pragma unroll
-        for (int k = 0; k < VPT; ++k)
+        for (int k = 0; k < VPT; ++k) {
+            const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
+            settle8<SF, WIDE>(xr[k], c, cols);
+            settle8<YF, WIDE>(yr[k], c, cols);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 x[k * 8 + e] = raw_at(xr[k], e);
                 y[k * 8 + e] = raw_at(yr[k], e);
             }
+        }
         if (a.has_y) {
             float r2 = 1.0f;
             if (a.post) {
@@ -237,11 +245,11 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
             r.y[k] = r.u[k] = Raw<YF>{};
             if (c < cols && row < last) {
                 if (a.pre) {
-                    load8<SF, WIDE>(r.x[k], row_of(a.x_out, row, a.ld_x_out, SF ? 4 : 2), c, cols);
-                    load8<YF, WIDE>(r.u[k], row_of(a.du, row, a.ld_du, YF ? 4 : 2), c, cols);
+                    fetch8<SF, WIDE>(r.x[k], row_of(a.x_out, row, a.ld_x_out, SF ? 4 : 2), c, cols);
+                    fetch8<YF, WIDE>(r.u[k], row_of(a.du, row, a.ld_du, YF ? 4 : 2), c, cols);
                 }
-                if (a.has_y) load8<YF, WIDE>(r.y[k], row_of(a.y, row, a.ld_y, YF ? 4 : 2), c, cols);
-                if (a.dx_out) load8<SF, WIDE>(r.d[k], row_of(a.dx_out, row, a.ld_dx_out, SF ? 4 : 2), c, cols);
+                if (a.has_y) fetch8<YF, WIDE>(r.y[k], row_of(a.y, row, a.ld_y, YF ? 4 : 2), c, cols);
+                if (a.dx_out) fetch8<SF, WIDE>(r.d[k], row_of(a.dx_out, row, a.ld_dx_out, SF ? 4 : 2), c, cols);
             }
         }
     };
@@ -321,7 +329,12 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
         }
         float s[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int k = 0; k < VPT; ++k)
+        for (int k = 0; k < VPT; ++k) {
+            const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
+            settle8<SF, WIDE>(r.x[k], c, cols);
+            settle8<SF, WIDE>(r.d[k], c, cols);
+            settle8<YF, WIDE>(r.y[k], c, cols);
+            settle8<YF, WIDE>(r.u[k], c, cols);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int i = k * 8 + e;
@@ -330,6 +343,7 @@ __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
                 s[1] += raw_at(r.u[k], e) * w_pre.get(i) * x;
                 s[2] += y * y;
             }
+        }
         block_join<Sum, THREADS, 3>(s, slots, turn);
         const float r1 = 1.0f / sqrtf(s[0] * inv_cols + a.eps_pre);
         const float m1 = s[1] * inv_cols * r1;          // mean(a * xh)
@@ -465,8 +479,9 @@ template <bool WIDE, int EPT, int THREADS>
 hipError_t launch_backward(const NormArgs &a, bool sf, bool yf, int64_t grid, hipStream_t s) {
     // The next row is loaded ahead where its rows are aligned and registers are
     // left for it (8192 x 8192 bf16: 122 us, 137 without; 4096 columns 67, 87).
-    // Unaligned rows end in a branch that the loads would wait at (8192 x 513:
-    // 32 us, 35 with the next row ahead).
+    // Unaligned rows need more registers as it is: float streams lose what bf16
+    // gains (4096 x 8191 in float 118 us, 137 with the next row ahead; 8192 x
+    // 8191 in bf16 199, 176).
     constexpr bool AHEAD = WIDE && !kOwnInLds<EPT, THREADS>;
     constexpr int lds = 2 * Own<EPT, THREADS, kOwnInLds<EPT, THREADS>>::BYTES;
     if (sf && yf) return launch_lds<norm_backward_kernel<WIDE, EPT, THREADS, true, true, AHEAD>>(grid, THREADS, lds, s, a);

@@ -58,23 +58,26 @@ __device__ __forceinline__ void *row_of(void *p, int64_t row, int64_t ld, int el
 
 // Columns c..c+7 of a row of `cols` (c < cols).  WIDE: the row starts on 16
 // bytes and cols is a multiple of 8.  Otherwise rows start on any element: the
-// same 16-byte accesses, which the hardware takes at any address, and the
-// row's last few columns one by one (the rest of them read as zero).
+// same 16-byte accesses, which the hardware takes at any address; a row's last
+// few columns come as the last 8 of the row (or one by one in a row of fewer),
+// which settle8 then shifts into place, zeros behind them.  It is a step of its
+// own so that all loads can go out before the first is waited for.
 typedef u32x4_t u32x4_at4_t __attribute__((aligned(4)));
 typedef u32x4_t u32x4_at2_t __attribute__((aligned(2)));
 typedef u32x2_t u32x2_at1_t __attribute__((aligned(1)));
 
 template <bool F32, bool WIDE>
-__device__ __forceinline__ void load8(Raw<F32> &r, const void *row, uint32_t c, uint32_t cols) {
-    if (WIDE || c + 8 <= cols) {
+__device__ __forceinline__ void fetch8(Raw<F32> &r, const void *row, uint32_t c, uint32_t cols) {
+    if (WIDE || cols >= 8) {
+        const uint32_t at = WIDE || c + 8 <= cols ? c : cols - 8;
         if constexpr (F32) {
             typedef std::conditional_t<WIDE, u32x4_t, u32x4_at4_t> words;
-            const words *q = (const words *)((const float *)row + c);
+            const words *q = (const words *)((const float *)row + at);
             r.a = q[0];
             r.b = q[1];
         } else {
             typedef std::conditional_t<WIDE, u32x4_t, u32x4_at2_t> words;
-            r.a = *(const words *)((const uint16_t *)row + c);
+            r.a = *(const words *)((const uint16_t *)row + at);
         }
     } else {
         r = Raw<F32>{};
@@ -90,6 +93,42 @@ __device__ __forceinline__ void load8(Raw<F32> &r, const void *row, uint32_t c, 
                 }
             }
     }
+}
+template <bool F32, bool WIDE>
+__device__ __forceinline__ void settle8(Raw<F32> &r, uint32_t c, uint32_t cols) {
+    if (WIDE || c + 8 <= cols || c >= cols || cols < 8) return;
+    const uint32_t by = c + 8 - cols;      // 1..7 elements
+    constexpr int N = F32 ? 8 : 4;
+    uint32_t w[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if constexpr (F32) w[i] = i < 4 ? r.a[i] : r.b[i - 4];
+        else w[i] = r.a[i];
+    }
+#pragma unroll
+    for (int step = 4; step >= 1; step >>= 1) {
+        if (!(by & step)) continue;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if constexpr (F32) w[i] = i + step < N ? w[i + step] : 0u;
+            else if (step > 1) w[i] = i + step / 2 < N ? w[i + step / 2] : 0u;
+            else w[i] = (w[i] >> 16) | (i + 1 < N ? w[i + 1] << 16 : 0u);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if constexpr (F32) {
+            if (i < 4) r.a[i] = w[i];
+            else r.b[i - 4] = w[i];
+        } else {
+            r.a[i] = w[i];
+        }
+    }
+}
+template <bool F32, bool WIDE>
+__device__ __forceinline__ void load8(Raw<F32> &r, const void *row, uint32_t c, uint32_t cols) {
+    fetch8<F32, WIDE>(r, row, c, cols);
+    settle8<F32, WIDE>(r, c, cols);
 }
 
 template <bool F32>

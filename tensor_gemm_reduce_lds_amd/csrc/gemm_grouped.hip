@@ -122,13 +122,77 @@ __device__ __forceinline__ bool find_row_tile(const GroupedArgs &p, int bm, uint
     return false;
 }
 
+// 8 columns of a row of C.  STREAM: a weight gradient, many times the caches'
+// size, is stored past them (6001 rows, 32 experts of 2048 x 1792 in 32 bits:
+// 165 us, streamed 129).
+template <bool WIDE, bool STREAM>
+__device__ __forceinline__ void store_run(const GroupedArgs &p, int64_t row, int64_t n, const int (&v)[8]) {
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = __int_as_float(v[e]);
+    const uint32_t at = (uint32_t)n, cols = (uint32_t)p.N;
+    void *const C = row_of(p.C, row, p.ldc, p.out_f32 ? 4 : 2);
+    if (p.out_f32) {
+        if (p.accumulate) {
+            Raw<true> c;
+            load8<true, WIDE>(c, C, at, cols);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] += raw_at(c, e);
+        }
+        store8<true, WIDE, STREAM>(C, at, cols, x);
+    } else {
+        if (p.accumulate) {
+            Raw<false> c;
+            load8<false, WIDE>(c, C, at, cols);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] += raw_at(c, e);
+        }
+        store8<false, WIDE, STREAM>(C, at, cols, x);
+    }
+}
+
+// Operands of 64 of the contraction in 128-byte LDS rows, for the kernels of
+// small tiles: 16-byte chunk c of row r sits at c ^ swz.  Row operand (a row of
+// the tile per output row): a lane's fragment of slice ks is 16 bytes of row
+// m + lane % 32.  Column operand (a row of the tile per row of the contraction):
+// two transposing reads, each of 4 rows of 4 chunks.
+__device__ __forceinline__ int row_swz(int r) { return (r ^ (r >> 3)) & 7; }
+__device__ __forceinline__ int col_swz(int r) { return 4 * ((r >> 1) & 1); }
+template <bool COL>
+__device__ __forceinline__ int swz(int r) { return COL ? col_swz(r) : row_swz(r); }
+template <bool COL>
+__device__ __forceinline__ i32x4_t fragment(lds_t *tile, int m, int ks) {
+    typedef __attribute__((address_space(3))) i32x4_t lds_i32x4;
+    typedef __attribute__((address_space(3))) i16x4_t lds_i16x4;
+    const int lane = threadIdx.x & 63;
+    if constexpr (COL) {
+        const int grp = lane >> 4, te = (lane & 15) >> 2, tq = lane & 3;
+        const int r = ks * 16 + 8 * (grp >> 1) + te, x = m + 16 * (grp & 1) + 4 * tq;
+        // rows r and r + 4 have the same swizzle
+        lds_t *const q = tile + r * 128 + (((x >> 3) ^ col_swz(r)) << 4) + ((x & 7) << 1);
+        const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)q);
+        const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(q + 4 * 128));
+        return __builtin_bit_cast(i32x4_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+        const int r = m + (lane & 31);
+        return *(lds_i32x4 *)(tile + r * 128 + (((2 * ks + (lane >> 5)) ^ row_swz(r)) << 4));
+    }
+}
+
 // Any size, stride and alignment, for what the others do not take: 64 x 64
-// outputs per workgroup, 32 x 32 per wave, 64 of the contraction at a time, elements one by one (coalesced along
-// the operand's contiguous axis, zeros outside it) into LDS rows of 144 bytes.
+// outputs per workgroup, 32 x 32 per wave, 64 of the contraction at a time,
+// loaded through registers (16 bytes at any element address, zeros outside the
+// operand) two steps ahead, and written to the other of two LDS buffers one step
+// ahead.  8000 rows, 64 experts of 4095 x 1791: product and gradient of x 500 us,
+// 235 TFLOP/s; loads of single elements took 2350.  Bound by the latency of a
+// step, as a tile of this size has few loads to run ahead.
 template <int OP>
 __global__ __launch_bounds__(256) void grouped_narrow_kernel(GroupedArgs p) {
-    constexpr int PITCH = 72;      // elements
-    __shared__ __attribute__((aligned(16))) uint16_t As[64 * PITCH], Bs[64 * PITCH];
+    constexpr bool A_COL = OP == GEMM_GROUPED_TN, B_COL = OP != GEMM_GROUPED_NT;
+    __shared__ __attribute__((aligned(1024))) char smem_generic[4 * 8192];
+    lds_t *const smem = (lds_t *)smem_generic;      // [buffer][operand]
+    typedef __attribute__((address_space(3))) u32x4_t lds_u32x4;
+    typedef __attribute__((address_space(3))) f32x4_t lds_f32x4;
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     if (blockIdx.x == 0 && wave == 0) check_offsets(p);
     int32_t lo = 0, hi;
@@ -141,6 +205,7 @@ __global__ __launch_bounds__(256) void grouped_narrow_kernel(GroupedArgs p) {
         group_rows(p, e, &lo, &hi);
         m0 = (int64_t)(t / p.tiles_n) * 64;
         n0 = (int64_t)(t % p.tiles_n) * 64;
+        if (hi == lo && p.accumulate) return;
         m_end = p.K;
         k_len = hi - lo;
     } else {
@@ -152,80 +217,82 @@ __global__ __launch_bounds__(256) void grouped_narrow_kernel(GroupedArgs p) {
         n0 = (int64_t)t.tn * 64;
         k_len = p.K;
     }
+    // this thread's chunks: number tid % 8 of rows tid / 8 and 32 further
+    const int chunk = tid & 7;
+    Raw<false> ra[2][2], rb[2][2];                  // of two steps
+    auto take = [&](Raw<false> &r, const uint16_t *at, int64_t ld, int64_t row, int64_t rows,
+                    int64_t from, int64_t upto) __attribute__((always_inline)) {
+        r = Raw<false>{};
+        if (row < rows && from + chunk * 8 < upto)
+            fetch8<false, false>(r, at + row * ld, (uint32_t)from + chunk * 8, (uint32_t)upto);
+    };
+    auto fetch = [&](int set, int64_t k0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = (tid >> 3) + 32 * i;
+            if constexpr (A_COL) take(ra[set][i], p.A + (int64_t)lo * p.lda, p.lda, k0 + r, k_len, m0, m_end);
+            else take(ra[set][i], p.A, p.lda, m0 + r, m_end, k0, k_len);
+            if constexpr (OP == GEMM_GROUPED_NN)
+                take(rb[set][i], p.B + (int64_t)e * p.K * p.ldb, p.ldb, k0 + r, k_len, n0, p.N);
+            else if constexpr (OP == GEMM_GROUPED_TN)
+                take(rb[set][i], p.B + (int64_t)lo * p.ldb, p.ldb, k0 + r, k_len, n0, p.N);
+            else take(rb[set][i], p.B + (int64_t)e * p.N * p.ldb, p.ldb, n0 + r, p.N, k0, k_len);
+        }
+    };
+    // (rows past an operand's hold zeros, which the shift leaves)
+    auto put = [&](int set, int64_t k0) __attribute__((always_inline)) {
+        const uint32_t a_from = (uint32_t)(A_COL ? m0 : k0) + chunk * 8, b_from = (uint32_t)(B_COL ? n0 : k0) + chunk * 8;
+        const uint32_t a_upto = (uint32_t)(A_COL ? m_end : k_len), b_upto = (uint32_t)(B_COL ? p.N : k_len);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = (tid >> 3) + 32 * i;
+            settle8<false, false>(ra[set][i], a_from, a_upto);
+            settle8<false, false>(rb[set][i], b_from, b_upto);
+            lds_t *const at = smem + set * 16384 + r * 128;
+            *(lds_u32x4 *)(at + ((chunk ^ swz<A_COL>(r)) << 4)) = ra[set][i].a;
+            *(lds_u32x4 *)(at + 8192 + ((chunk ^ swz<B_COL>(r)) << 4)) = rb[set][i].a;
+        }
+    };
     const int wm = (wave >> 1) * 32, wn = (wave & 1) * 32;
     f32x16_t acc = {};
-    for (int64_t k0 = 0; k0 < k_len; k0 += 64) {
-#pragma unroll 4
-        for (int i = 0; i < 16; ++i) {
-            const int fast = tid & 63, slow = i * 4 + (tid >> 6);
-            uint16_t av = 0, bv = 0;
-            // A
-            const int am = OP == GEMM_GROUPED_TN ? fast : slow, ak = OP == GEMM_GROUPED_TN ? slow : fast;
-            if (m0 + am < m_end && k0 + ak < k_len)
-                av = OP == GEMM_GROUPED_TN ? p.A[(lo + k0 + ak) * p.lda + m0 + am]
-                                           : p.A[(m0 + am) * p.lda + k0 + ak];
-            As[am * PITCH + ak] = av;
-            const int bn = OP == GEMM_GROUPED_NT ? slow : fast, bk = OP == GEMM_GROUPED_NT ? fast : slow;
-            if (n0 + bn < p.N && k0 + bk < k_len)
-                bv = OP == GEMM_GROUPED_NN   ? p.B[((int64_t)e * p.K + k0 + bk) * p.ldb + n0 + bn]
-                     : OP == GEMM_GROUPED_NT ? p.B[((int64_t)e * p.N + n0 + bn) * p.ldb + k0 + bk]
-                                             : p.B[(lo + k0 + bk) * p.ldb + n0 + bn];
-            Bs[bn * PITCH + bk] = bv;
-        }
-        __syncthreads();
+    fetch(0, 0);
+    fetch(1, 64);                                   // (nothing past the end)
+    put(0, 0);
+    lds_only_barrier();
+    // the step at k0, in buffer `now`
+    auto step = [&](int now, int64_t k0) __attribute__((always_inline)) {
+        fetch(now, k0 + 128);
+        lds_t *const at = smem + now * 16384;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int c = s * 16 + (lane >> 5) * 8;
-            acc = mma(*(const i32x4_t *)(As + (wm + (lane & 31)) * PITCH + c),
-                      *(const i32x4_t *)(Bs + (wn + (lane & 31)) * PITCH + c), acc);
-        }
-        __syncthreads();
+        for (int ks = 0; ks < 4; ++ks)
+            acc = mma(fragment<A_COL>(at, wm, ks), fragment<B_COL>(at + 8192, wn, ks), acc);
+        put(now ^ 1, k0 + 64);
+        lds_only_barrier();
+    };
+    for (int64_t k0 = 0; k0 < k_len; k0 += 128) {
+        step(0, k0);
+        if (k0 + 64 < k_len) step(1, k0 + 64);
     }
-    const int64_t m = m0 + wm + (lane & 31);
-    const int64_t out0 = OP == GEMM_GROUPED_TN ? ((int64_t)e * p.K + m) * p.ldc : m * p.ldc;
+    // through LDS, so that runs of 8 columns are stored together
+    const int m = wm + (lane & 31);
 #pragma unroll
-    for (int v = 0; v < 16; ++v) {
-        const int64_t n = n0 + wn + 8 * (v >> 2) + 4 * (lane >> 5) + (v & 3);
-        if (m < m_end && n < p.N) {
-            float x = acc[v];
-            if (p.out_f32) {
-                float *c = (float *)p.C + out0 + n;
-                *c = p.accumulate ? *c + x : x;
-            } else {
-                uint16_t *c = (uint16_t *)p.C + out0 + n;
-                if (p.accumulate) x += bf16_lo(*c);
-                *c = (uint16_t)to_bf16(x);
-            }
-        }
+    for (int q = 0; q < 4; ++q) {
+        const f32x4_t v = {acc[4 * q], acc[4 * q + 1], acc[4 * q + 2], acc[4 * q + 3]};
+        *(lds_f32x4 *)(smem + m * 256 + (((wn / 4 + 2 * q + (lane >> 5)) ^ (m & 15)) << 4)) = v;
     }
-}
-
-// 8 columns of a row of C.  STREAM: a weight gradient, many times the caches'
-// size, is stored past them (6001 rows, 32 experts of 2048 x 1792 in 32 bits:
-// 165 us, streamed 129).
-template <bool STREAM>
-__device__ __forceinline__ void store_run(const GroupedArgs &p, int64_t row, int64_t n, const int (&v)[8]) {
-    float x[8];
+    lds_only_barrier();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = __int_as_float(v[e]);
-    const uint32_t at = (uint32_t)n, cols = (uint32_t)p.N;
-    void *const C = row_of(p.C, row, p.ldc, p.out_f32 ? 4 : 2);
-    if (p.out_f32) {
-        if (p.accumulate) {
-            Raw<true> c;
-            load8<true, true>(c, C, at, cols);
+    for (int i = 0; i < 2; ++i) {
+        const int r = (tid >> 3) + 32 * i, c = chunk * 8;
+        if (m0 + r >= m_end || n0 + c >= p.N) continue;
+        int v[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] += raw_at(c, e);
+        for (int h = 0; h < 2; ++h) {
+            const f32x4_t x = *(lds_f32x4 *)(smem + r * 256 + (((2 * chunk + h) ^ (r & 15)) << 4));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) v[4 * h + u] = __float_as_int(x[u]);
         }
-        store8<true, true, STREAM>(C, at, cols, x);
-    } else {
-        if (p.accumulate) {
-            Raw<false> c;
-            load8<false, true>(c, C, at, cols);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] += raw_at(c, e);
-        }
-        store8<false, true, STREAM>(C, at, cols, x);
+        store_run<false, false>(p, (OP == GEMM_GROUPED_TN ? (int64_t)e * p.K : 0) + m0 + r, n0 + c, v);
     }
 }
 
@@ -285,7 +352,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_tile_kernel(GroupedArg
         const Operand b = {(const char *)(p.B + (int64_t)lo * p.ldb + n0), p.ldb * 2, n_left * 2};
         tile.template run<2>(smem, a, b, hi - lo);
         tile.store(smem, [&](int r, int c, const int (&v)[8]) {
-            if (r < m_left && c < n_left) store_run<true>(out, (int64_t)e * p.K + m0 + r, n0 + c, v);
+            if (r < m_left && c < n_left) store_run<true, true>(out, (int64_t)e * p.K + m0 + r, n0 + c, v);
         });
     } else {
         RowTile t;
@@ -295,7 +362,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_tile_kernel(GroupedArg
         const int32_t n_left = (int32_t)(p.N - n0 < BN ? p.N - n0 : BN);
         tile.template run<2>(smem, row_operand(p, t, m_left), column_operand<OP>(p, t.e, n0, n_left), (int32_t)p.K);
         tile.store(smem, [&](int r, int c, const int (&v)[8]) {
-            if (r < m_left && c < n_left) store_run<false>(p, (int64_t)t.row0 + r, n0 + c, v);
+            if (r < m_left && c < n_left) store_run<true, false>(p, (int64_t)t.row0 + r, n0 + c, v);
         });
     }
 }
@@ -315,11 +382,6 @@ struct StreamTile {
     static_assert(BN == 64, "B's rows of a stage are 128 bytes in both forms");
     static_assert(LDS_BYTES <= 160 * 1024 && BM * BN * 4 <= S * STAGE, "LDS");
     static_assert((S - 1) * LOADS < 64, "the load counter");
-
-    // 16-byte chunk c of row r of a stage's tile sits at c ^ swz.  B in NN (r: a
-    // row of the contraction): a transposing read takes 4 rows of 4 chunks.
-    static __device__ __forceinline__ int row_swz(int r) { return (r ^ (r >> 3)) & 7; }
-    static __device__ __forceinline__ int col_swz(int r) { return 4 * ((r >> 1) & 1); }
 
     template <class F>
     static __device__ __forceinline__ void run(lds_t *smem, const Operand &a, const Operand &b, int32_t K, F store) {
@@ -342,7 +404,7 @@ struct StreamTile {
             for (int i = 0; i < LOADS; ++i) {
                 const bool isb = i >= A_LOADS;
                 const int r = (isb ? i - A_LOADS : i) * 8 + lr;
-                const int c = lc ^ (isb && COL ? col_swz(r) : row_swz(r));
+                const int c = lc ^ (isb ? swz<COL>(r) : row_swz(r));
                 uint32_t v = (uint32_t)r * (uint32_t)(isb ? b.ld : a.ld) + c * 16;
                 // past the contraction's end: rows of NN's B lie past the
                 // descriptor, chunks of the others are sent there
@@ -350,13 +412,10 @@ struct StreamTile {
                 load_to_lds(isb ? rb : ra, v, own_base + st * STAGE + i * 1024);
             }
         };
-        typedef __attribute__((address_space(3))) i32x4_t lds_i32x4;
-        typedef __attribute__((address_space(3))) i16x4_t lds_i16x4;
         typedef __attribute__((address_space(3))) f32x4_t lds_f32x4;
         f32x16_t acc[FN];
 #pragma unroll
         for (int j = 0; j < FN; ++j) acc[j] = f32x16_t{};
-        const int grp = lane >> 4, te = (lane & 15) >> 2, tq = lane & 3;
 #pragma unroll
         for (int s = 0; s < S - 1; ++s)
             if (s < mine) issue(s, s);
@@ -367,25 +426,9 @@ struct StreamTile {
             lds_t *const at = own + st * STAGE, *const bt = at + A_BYTES;
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-                i32x4_t bf[FN];
-                const int m = lane & 31;
-                const i32x4_t af = *(lds_i32x4 *)(at + m * 128 + (((2 * ks + (lane >> 5)) ^ row_swz(m)) << 4));
+                const i32x4_t af = fragment<false>(at, 0, ks);
 #pragma unroll
-                for (int j = 0; j < FN; ++j) {
-                    if constexpr (COL) {
-                        const int r = ks * 16 + 8 * (grp >> 1) + te, x = j * 32 + 16 * (grp & 1) + 4 * tq;
-                        // rows r and r + 4 have the same swizzle
-                        lds_t *const q = bt + r * 128 + (((x >> 3) ^ col_swz(r)) << 4) + ((x & 7) << 1);
-                        const i16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)q);
-                        const i16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4 *)(q + 4 * 128));
-                        bf[j] = __builtin_bit_cast(i32x4_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-                    } else {
-                        const int r = j * 32 + (lane & 31);
-                        bf[j] = *(lds_i32x4 *)(bt + r * 128 + (((2 * ks + (lane >> 5)) ^ row_swz(r)) << 4));
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < FN; ++j) acc[j] = mma(af, bf[j], acc[j]);
+                for (int j = 0; j < FN; ++j) acc[j] = mma(af, fragment<COL>(bt, j * 32, ks), acc[j]);
             }
             // the reads are done before the next issue overwrites their stage
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -431,7 +474,7 @@ __global__ __launch_bounds__(StreamTile<OP>::THREADS) void grouped_stream_kernel
     const int32_t n_left = (int32_t)(p.N - n0 < T::BN ? p.N - n0 : T::BN);
     T::run((lds_t *)smem_generic, row_operand(p, t, m_left), column_operand<OP>(p, t.e, n0, n_left),
            (int32_t)p.K, [&](int r, int c, const int (&v)[8]) {
-               if (r < m_left && c < n_left) store_run<false>(p, (int64_t)t.row0 + r, n0 + c, v);
+               if (r < m_left && c < n_left) store_run<true, false>(p, (int64_t)t.row0 + r, n0 + c, v);
            });
 }
 
@@ -470,7 +513,7 @@ __global__ __launch_bounds__(256) void grouped_join_kernel(GroupedArgs p) {
         int v[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = __float_as_int(x[e]);
-        store_run<false>(p, row, n, v);
+        store_run<true, false>(p, row, n, v);
     }
 }
 

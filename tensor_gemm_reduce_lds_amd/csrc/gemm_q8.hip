@@ -208,9 +208,10 @@ __global__ __launch_bounds__(THREADS) void quantize_kernel(const void *x, int64_
         float m[1] = {0.0f};
         auto take = [&](Raw<F32> &r, uint32_t c) {
             r = Raw<F32>{};
-            if (c < cols) load8<F32, WIDE>(r, from, c, cols);
+            if (c < cols) fetch8<F32, WIDE>(r, from, c, cols);
         };
-        auto look = [&](const Raw<F32> &r) {
+        auto look = [&](Raw<F32> &r, uint32_t c) {
+            settle8<F32, WIDE>(r, c, cols);
 #pragma unroll
             for (int e = 0; e < 8; ++e) m[0] = MaxBits::join(m[0], fabsf(raw_at(r, e)));
         };
@@ -218,11 +219,11 @@ __global__ __launch_bounds__(THREADS) void quantize_kernel(const void *x, int64_
 #pragma unroll
             for (int k = 0; k < VPT; ++k) take(held[k], t0 + k * THREADS * 8);
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) look(held[k]);
+            for (int k = 0; k < VPT; ++k) look(held[k], t0 + k * THREADS * 8);
         } else {
             for (uint32_t c = t0; c < cols; c += THREADS * 8) {
                 take(held[0], c);
-                look(held[0]);
+                look(held[0], c);
             }
         }
         block_join<MaxBits, THREADS, 1>(m, slots, turn);
@@ -239,6 +240,7 @@ __global__ __launch_bounds__(THREADS) void quantize_kernel(const void *x, int64_
         } else {
             for (uint32_t c = t0; c < padded; c += THREADS * 8) {
                 take(held[0], c);
+                settle8<F32, WIDE>(held[0], c, cols);
                 put(held[0], c);
             }
         }
