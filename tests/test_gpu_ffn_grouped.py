@@ -120,6 +120,31 @@ def test_large_groups(op):
             _run(op, sizes, N, K, ternary=ternary)
 
 
+MANY = [90, 0, 141, 80] * 10
+
+
+@pytest.mark.parametrize("op", list(OPS))
+@pytest.mark.parametrize("sizes,N,K", [(MANY, 520, 72), (MANY, 776, 136), (MANY, 1032, 72), (MANY, 1032, 1032), ([3300, 1, 2900], 2056, 520),
+                                       ([1100, 0, 37, 900], 264, 72), ([5000], 264, 136), ([700, 0, 301], 257, 131)],
+                         ids=lambda v: str(sum(v)) if isinstance(v, list) else str(v))
+def test_every_tile(op, sizes, N, K):
+    """Numbers of tiles from a few to several rounds, so that each tile of the
+    rules runs, with rows and columns that end inside it."""
+    say("grouped tiles", op, len(sizes), sum(sizes), N, K)
+    _run(op, sizes, N, K, seed=K)
+    _run(op, sizes, N, K, out=F.F32, pads=(8, 16, 24), ternary=True, seed=N)
+
+
+@pytest.mark.parametrize("op", list(OPS))
+@pytest.mark.parametrize("end", range(1, 8))
+def test_row_ends_of_every_length(op, end):
+    """Rows that end 1..7 elements past a multiple of 8, and rows of fewer than 8."""
+    for N, K in ((64 + end, 128 + end), (end, 72 + end), (72 + end, end)):
+        say("grouped ends", op, N, K)
+        _run(op, [70, 0, 9], N, K, pads=(1, 2, 3))
+        _run(op, [70, 0, 9], N, K, out=F.F32, ternary=True)
+
+
 @pytest.mark.parametrize("op", list(OPS))
 def test_rows_outside_groups_strides_and_alignment(op):
     for kw in (dict(first=5, capacity=400), dict(rows=350, capacity=400), dict(first=130, rows=460, capacity=460),

@@ -216,6 +216,26 @@ def test_backward(rows, cols, types):
     _backward(Case(rows, cols, *types, rpg=2, seed=rows + cols, backward=1))
 
 
+@pytest.mark.parametrize("types", TYPES, ids=["bb", "bf", "fb", "ff"])
+@pytest.mark.parametrize("end", range(1, 8))
+def test_row_ends_of_every_length(end, types):
+    """Rows that end 1..7 elements past a multiple of 8, and rows of fewer than 8."""
+    for cols in (end, 8 + end, 512 + end):
+        for pad in (0, 3):
+            say("norm ends", cols, types)
+            _forward(Case(3, cols, *types, rpg=2, pad=pad, seed=cols))
+            _backward(Case(3, cols, *types, rpg=2, pad=pad, seed=cols, backward=1))
+
+
+@pytest.mark.parametrize("rows,cols", [(260, 4104), (257, 8191), (1100, 2056)])
+def test_many_rows(rows, cols):
+    """More rows than CUs, where long rows take fewer threads each, and more than
+    the workgroups of a backward launch."""
+    say("norm many rows", rows, cols)
+    _forward(Case(rows, cols, rpg=100))
+    _backward(Case(rows, cols, rpg=100, backward=1))
+
+
 @pytest.mark.parametrize("kw", VARIANTS, ids=str)
 @pytest.mark.parametrize("cols", [320, 4097])
 def test_backward_variants(cols, kw):

@@ -75,6 +75,24 @@ def test_product(M, N, K, out, bias):
     _product(M, N, K, out, bias, seed=M + N + K)
 
 
+@pytest.mark.parametrize("M,N", [(65, 264), (3300, 264), (6000, 264), (700, 6152), (6000, 1034), (2100, 4104)])
+def test_every_tile(M, N):
+    """Numbers of tiles from a few to several rounds, so that each tile of the
+    rule runs, with rows and columns that end inside it."""
+    say("q8 tiles", M, N)
+    _product(M, N, 80, F.BF16, seed=M)
+    _product(M, N, 80, F.F32, ldd=N + 3, seed=N)
+
+
+@pytest.mark.parametrize("end", range(1, 8))
+def test_row_ends_of_every_length(end):
+    for M in (3, 70):
+        for N in (64 + end, end):
+            say("q8 ends", M, N)
+            _product(M, N, 48, F.BF16, seed=N)
+            _product(M, N, 48, F.F32, bias=True, seed=N)
+
+
 @pytest.mark.parametrize("M", [1, 5, 40, 200, 700])
 def test_strides_fewer_rows_and_unaligned_output(M):
     say("q8 strides", M)
@@ -127,6 +145,14 @@ def test_quantize_equals_the_stated_float_steps(dtype, rows, cols, ldx, ldq):
     assert np.array_equal(s, want_s, equal_nan=True)
     assert np.array_equal(q[:, :cols], want_q)
     assert not q[:, cols:padded].any() and (q[:, padded:] == 77).all()
+
+
+@pytest.mark.parametrize("dtype", [F.BF16, F.F32])
+@pytest.mark.parametrize("end", range(1, 8))
+def test_quantize_row_ends_of_every_length(dtype, end):
+    for cols in (end, 8 + end, 512 + end, 2048 + end, 16384 + end):
+        say("quantize ends", cols)
+        test_quantize_equals_the_stated_float_steps(dtype, 4, cols, cols + 1, 0)
 
 
 def test_quantize_tiny_rows():
