@@ -137,42 +137,40 @@ __device__ __forceinline__ float raw_at(const Raw<F32> &r, int e) {
     else return (e & 1) ? bf16_hi(r.a[e >> 1]) : bf16_lo(r.a[e >> 1]);
 }
 
-// The same columns written; STREAM: past the caches.
+// Columns c..c+3 of a row of `cols` floats (c < cols), aligned as above; STREAM:
+// past the caches.
+template <bool WIDE, bool STREAM = false>
+__device__ __forceinline__ void store4(float *row, uint32_t c, uint32_t cols, const float *v) {
+    if (WIDE || c + 4 <= cols) {
+        typedef std::conditional_t<WIDE, u32x4_t, u32x4_at4_t> words;
+        u32x4_t w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(v[e]);
+        if constexpr (STREAM) __builtin_nontemporal_store(w, (words *)(row + c));
+        else *(words *)(row + c) = w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            if (c + e < cols) row[c + e] = v[e];
+    }
+}
+// Columns c..c+7, of either type.
 template <bool F32, bool WIDE, bool STREAM = false>
 __device__ __forceinline__ void store8(void *row, uint32_t c, uint32_t cols, const float *v) {
-    if (WIDE || c + 8 <= cols) {
-        if constexpr (F32) {
-            typedef std::conditional_t<WIDE, u32x4_t, u32x4_at4_t> words;
-            words *q = (words *)((float *)row + c);
-            u32x4_t a, b;
+    if constexpr (F32) {
+        store4<WIDE, STREAM>((float *)row, c, cols, v);
+        if (WIDE || c + 4 < cols) store4<WIDE, STREAM>((float *)row, c + 4, cols, v + 4);
+    } else if (WIDE || c + 8 <= cols) {
+        typedef std::conditional_t<WIDE, u32x4_t, u32x4_at2_t> words;
+        u32x4_t w;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                a[e] = __float_as_uint(v[e]);
-                b[e] = __float_as_uint(v[e + 4]);
-            }
-            if constexpr (STREAM) {
-                __builtin_nontemporal_store(a, q);
-                __builtin_nontemporal_store(b, q + 1);
-            } else {
-                q[0] = a;
-                q[1] = b;
-            }
-        } else {
-            typedef std::conditional_t<WIDE, u32x4_t, u32x4_at2_t> words;
-            words *q = (words *)((uint16_t *)row + c);
-            u32x4_t w;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-            if constexpr (STREAM) __builtin_nontemporal_store(w, q);
-            else *q = w;
-        }
+        for (int e = 0; e < 4; ++e) w[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+        if constexpr (STREAM) __builtin_nontemporal_store(w, (words *)((uint16_t *)row + c));
+        else *(words *)((uint16_t *)row + c) = w;
     } else {
 #pragma unroll
         for (int e = 0; e < 7; ++e)
-            if (c + e < cols) {
-                if constexpr (F32) ((float *)row)[c + e] = v[e];
-                else ((uint16_t *)row)[c + e] = (uint16_t)to_bf16(v[e]);
-            }
+            if (c + e < cols) ((uint16_t *)row)[c + e] = (uint16_t)to_bf16(v[e]);
     }
 }
 

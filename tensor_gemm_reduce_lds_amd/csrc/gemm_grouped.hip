@@ -7,9 +7,10 @@
 //
 // Bound by the matrix pipe at the board's power limit where experts have many
 // rows (16384 rows, 8 experts of 4096 x 3584: product 437 us, 1100 TFLOP/s,
-// gradients 466 and 423 us), by reading B or writing weight gradients where they
+// gradients 466 and 420 us), by reading B or writing weight gradients where they
 // have few (8000 rows, 64 experts of 4096 x 1792: 220 us, 4.7 TB/s; 128 rows, 8
-// experts of 4096 x 3584: 44 us, 5.4 TB/s, part of it from the caches).
+// experts of 4096 x 3584: 44 us, 5.4 TB/s, part of it from the caches; gradients
+// of 44 experts of 4040 x 2048 in 32 bits, 164 rows: 223 us, 6.5 TB/s).
 #include <math.h>
 #include <stdlib.h>
 
@@ -33,6 +34,7 @@ struct GroupedArgs {
     int32_t *err;
     int32_t parts;                // TN: workgroups that share a tile's contraction
     float *slots;                 // their sums, [part][E][K][N] (parts > 1)
+    int32_t stream;               // TN: C is stored past the caches
 };
 
 // Rows [lo, hi) of expert e, clipped to 0 <= lo <= hi <= rows.
@@ -122,33 +124,47 @@ __device__ __forceinline__ bool find_row_tile(const GroupedArgs &p, int bm, uint
     return false;
 }
 
-// 8 columns of a row of C.  STREAM: a weight gradient, many times the caches'
-// size, is stored past them (6001 rows, 32 experts of 2048 x 1792 in 32 bits:
-// 165 us, streamed 129).
+// 4 or 8 columns of a row of C; STREAM: past the caches.
+template <bool WIDE, bool STREAM>
+__device__ __forceinline__ void store_four(const GroupedArgs &p, int64_t row, int64_t n, const int *v) {
+    float x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = __int_as_float(v[e]);
+    float *const C = (float *)row_of(p.C, row, p.ldc, 4);
+    const uint32_t at = (uint32_t)n, cols = (uint32_t)p.N;
+    if (p.accumulate) {
+        typedef std::conditional_t<WIDE, u32x4_t, u32x4_at4_t> words;
+        if (WIDE || at + 4 <= cols) {
+            const u32x4_t c = *(const words *)(C + at);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] += __uint_as_float(c[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 3; ++e)
+                if (at + e < cols) x[e] += C[at + e];
+        }
+    }
+    store4<WIDE, STREAM>(C, at, cols, x);
+}
 template <bool WIDE, bool STREAM>
 __device__ __forceinline__ void store_run(const GroupedArgs &p, int64_t row, int64_t n, const int (&v)[8]) {
+    if (p.out_f32) {
+        store_four<WIDE, STREAM>(p, row, n, v);
+        if (WIDE || n + 4 < p.N) store_four<WIDE, STREAM>(p, row, n + 4, v + 4);
+        return;
+    }
     float x[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = __int_as_float(v[e]);
     const uint32_t at = (uint32_t)n, cols = (uint32_t)p.N;
-    void *const C = row_of(p.C, row, p.ldc, p.out_f32 ? 4 : 2);
-    if (p.out_f32) {
-        if (p.accumulate) {
-            Raw<true> c;
-            load8<true, WIDE>(c, C, at, cols);
+    void *const C = row_of(p.C, row, p.ldc, 2);
+    if (p.accumulate) {
+        Raw<false> c;
+        load8<false, WIDE>(c, C, at, cols);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] += raw_at(c, e);
-        }
-        store8<true, WIDE, STREAM>(C, at, cols, x);
-    } else {
-        if (p.accumulate) {
-            Raw<false> c;
-            load8<false, WIDE>(c, C, at, cols);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] += raw_at(c, e);
-        }
-        store8<false, WIDE, STREAM>(C, at, cols, x);
+        for (int e = 0; e < 8; ++e) x[e] += raw_at(c, e);
     }
+    store8<false, WIDE, STREAM>(C, at, cols, x);
 }
 
 // Operands of 64 of the contraction in 128-byte LDS rows, for the kernels of
@@ -312,6 +328,21 @@ __device__ __forceinline__ Operand column_operand(const GroupedArgs &p, int e, i
         return {(const char *)(p.B + ((int64_t)e * p.N + n0) * p.ldb), p.ldb * 2, cols};
 }
 
+// A tile's m_left x n_left (columns: a multiple of 8) outputs from row m0 and column n0 of C.
+template <bool STREAM, class T>
+__device__ __forceinline__ void store_tile(const GroupedArgs &p, const T &tile, lds_t *smem, int64_t m0, int32_t m_left,
+                                           int64_t n0, int32_t n_left) {
+    if (p.out_f32)
+        tile.template store<true>(smem, [&](int r, int c, int d, const int (&v)[8]) {
+            if (r < m_left && c < n_left) store_four<true, STREAM>(p, m0 + r, n0 + c, v);
+            if (r < m_left && d < n_left) store_four<true, STREAM>(p, m0 + r, n0 + d, v + 4);
+        });
+    else
+        tile.template store<false>(smem, [&](int r, int c, int, const int (&v)[8]) {
+            if (r < m_left && c < n_left) store_run<true, STREAM>(p, m0 + r, n0 + c, v);
+        });
+}
+
 template <int OP, int BM, int BN, int WGM, int WGN, int SA, int SB>
 __global__ __launch_bounds__(64 * WGM * WGN) void grouped_tile_kernel(GroupedArgs p) {
     using T = GroupedTile<OP, BM, BN, WGM, WGN, SA, SB>;
@@ -351,9 +382,8 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_tile_kernel(GroupedArg
         const Operand a = {(const char *)(p.A + (int64_t)lo * p.lda + m0), p.lda * 2, m_left * 2};
         const Operand b = {(const char *)(p.B + (int64_t)lo * p.ldb + n0), p.ldb * 2, n_left * 2};
         tile.template run<2>(smem, a, b, hi - lo);
-        tile.store(smem, [&](int r, int c, const int (&v)[8]) {
-            if (r < m_left && c < n_left) store_run<true, true>(out, (int64_t)e * p.K + m0 + r, n0 + c, v);
-        });
+        if (p.stream) store_tile<true>(out, tile, smem, (int64_t)e * p.K + m0, m_left, n0, n_left);
+        else store_tile<false>(out, tile, smem, (int64_t)e * p.K + m0, m_left, n0, n_left);
     } else {
         RowTile t;
         if (!find_row_tile(p, BM, blockIdx.x, &t)) return;
@@ -361,9 +391,7 @@ __global__ __launch_bounds__(64 * WGM * WGN) void grouped_tile_kernel(GroupedArg
         const int32_t m_left = t.end - t.row0 < BM ? t.end - t.row0 : BM;
         const int32_t n_left = (int32_t)(p.N - n0 < BN ? p.N - n0 : BN);
         tile.template run<2>(smem, row_operand(p, t, m_left), column_operand<OP>(p, t.e, n0, n_left), (int32_t)p.K);
-        tile.store(smem, [&](int r, int c, const int (&v)[8]) {
-            if (r < m_left && c < n_left) store_run<true, false>(p, (int64_t)t.row0 + r, n0 + c, v);
-        });
+        store_tile<false>(p, tile, smem, t.row0, m_left, n0, n_left);
     }
 }
 
@@ -578,14 +606,13 @@ hipError_t launch_rows(GroupedArgs &a, hipStream_t s) {
 
 // TN: 256 x 256 tiles, or 128 x 128 with two workgroups per CU, so that one
 // stores while the other loads: better for short groups, whose time is the
-// stores (us for 256 / 128: 188 rows per expert 158 / 126, 2048 rows 431 / 556),
-// and where there are fewer large tiles than CUs, unless those run in one round
-// and the small ones do not (118 rows, 3480 x 1240, 2 experts in 32 bits: 13 /
-// 18).  With few of the small ones too, `parts` workgroups share a tile's rows
-// and a second kernel adds them, as many as take the least time, from about 0.5
-// us per step of 64 rows, and for the second kernel 4 us and the parts' traffic
-// (16030 rows, 1296 x 304, 2 experts: 1 part 76 us, 4 39, 8 36, 16 41; 7984 rows,
-// 768 x 512, 8 experts: 1 part 20 us, 2 26).
+// stores (us for 256 / 128: 190 rows per expert, 17 experts of 3136 x 1408 in 32
+// bits 84 / 73; 2048 rows, 8 experts of 4096 x 3584 422 / 565), and where there
+// are fewer large tiles than CUs.  With few of the small ones too, `parts`
+// workgroups share a tile's rows and a second kernel adds them, as many as take
+// the least time, from about 0.5 us per step of 64 rows, and for the second
+// kernel 4 us and the parts' traffic (16030 rows, 1296 x 304, 2 experts: 1 part 76
+// us, 4 38, 8 32; 7984 rows, 768 x 512, 8 experts: 1 part 20 us, 2 26).
 struct TnChoice {
     bool large;
     int parts;
@@ -593,7 +620,7 @@ struct TnChoice {
 TnChoice tn_choice(int64_t rows, int64_t K, int64_t N, int64_t E) {
     const int64_t large = E * ((K + 255) / 256) * ((N + 255) / 256);
     const int64_t small = E * ((K + 127) / 128) * ((N + 127) / 128);
-    if (large >= kCus ? rows / E >= 448 : small > 2 * kCus) return {true, 1};
+    if (large >= kCus && rows / E >= 448) return {true, 1};
     const double steps = (double)(rows / E) / 64, part_us = (double)E * K * N * 8 / 6.0e6;
     int parts = 1;
     double best_us = 0.5 * steps;
@@ -606,8 +633,20 @@ TnChoice tn_choice(int64_t rows, int64_t K, int64_t N, int64_t E) {
     }
     return {false, parts};
 }
+// Weight gradients are many times the caches' size, so they are stored past them,
+// and the caches keep the rows (6001 rows, 32 experts of 2048 x 1792 in 32 bits:
+// 111 us, 165 through them; 164 rows, 44 experts of 4040 x 2048: 223, 292).  Such
+// stores have to cover whole lines (in runs of half a line: 589).  Rows that do
+// not begin on a line break that at each tile's edge, which in 32 bits costs more
+// than few rows per expert gain (20 experts of 1280 x 3576, 32 rows each 115 / 79,
+// 64 rows 114 / 102, 128 rows 112 / 132; in bfloat16 56 / 50, 60 / 58, 74 / 70,
+// but 34 experts of 3648 x 2248, 84 rows each 175 / 234).
+bool stream_stores(const GroupedArgs &a) {
+    return !a.out_f32 || (a.ldc % 32 == 0 && aligned(a.C, 128)) || a.rows / a.E >= 96;
+}
 hipError_t launch_tn(GroupedArgs &a, int max_parts, hipStream_t s) {
     const TnChoice c = tn_choice(a.rows, a.K, a.N, a.E);
+    a.stream = stream_stores(a);
     if (c.large) return launch_tile<GEMM_GROUPED_TN, 256, 256, 2, 4, 2, 2>(a, s);
     a.parts = c.parts < max_parts ? c.parts : max_parts;    // (the slots hold max_parts)
     hipError_t e = launch_tile<GEMM_GROUPED_TN, 128, 128, 2, 2, 2, 3>(a, s);

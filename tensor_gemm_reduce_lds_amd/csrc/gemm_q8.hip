@@ -31,6 +31,43 @@ __device__ __forceinline__ void store_one(const Q8Args &p, int64_t m, int64_t n,
     else ((uint16_t *)p.D)[m * p.ldd + n] = (uint16_t)to_bf16(v);
 }
 
+// A tile's sums from row m0 and column n0 on, scaled and stored.  A lane's columns
+// are the same in every row it stores.
+template <bool F32, class T>
+__device__ __forceinline__ void store_tile(const Q8Args &p, const T &tile, lds_t *smem, int64_t m0, int32_t m_left, int64_t n0,
+                                           int32_t n_left) {
+    const int lane = (int)(threadIdx.x % (T::BN / 8));
+    const int from[2] = {F32 ? lane * 4 : lane * 8, F32 ? lane * 4 + T::BN / 2 : lane * 8 + 4};
+    float sw[8], bias[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int64_t c = n0 + from[e / 4] + e % 4, n = c < p.N ? c : p.N - 1;
+        sw[e] = p.w_scale[n];
+        bias[e] = p.bias ? p.bias[n] : 0.0f;
+    }
+    const uint32_t cols = (uint32_t)p.N;
+    tile.template store<F32>(smem, [&](int r, int c, int d, const int (&v)[8]) {
+        if (r >= m_left || c >= n_left) return;
+        const int64_t m = m0 + r;
+        const float sa = p.a_scale[m];
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = scaled(v[e], sa, sw[e], p.bias ? &bias[e] : nullptr);
+        void *const to = row_of(p.D, m, p.ldd, F32 ? 4 : 2);
+        const uint32_t at = (uint32_t)(n0 + c), next = (uint32_t)(n0 + d);
+        if constexpr (F32) {
+            if (p.wide_out) store4<true>((float *)to, at, cols, x);
+            else store4<false>((float *)to, at, cols, x);
+            if (d >= n_left) return;
+            if (p.wide_out) store4<true>((float *)to, next, cols, x + 4);
+            else store4<false>((float *)to, next, cols, x + 4);
+        } else {
+            if (p.wide_out) store8<false, true>(to, at, cols, x);
+            else store8<false, false>(to, at, cols, x);
+        }
+    });
+}
+
 // BM x BN outputs per workgroup.  An XCD gets a run of the tiles in groups of 8
 // tile-rows, a group column by column.  8192 x 8192 x 3584: 236 us, 2040 TOP/s (a
 // library product of 8192^3 on the same card runs at 2260), at the board's power
@@ -51,32 +88,8 @@ __global__ __launch_bounds__(64 * WGM * WGN) void q8_tile_kernel(Q8Args p) {
     const Operand a = {(const char *)p.a + m0 * p.lda, p.lda, m_left};
     const Operand w = {(const char *)p.w + n0 * p.ldw, p.ldw, n_left};
     tile.template run<1>(smem, a, w, (int32_t)p.K);
-    // a lane's 8 columns are the same in every row it stores
-    const int c0 = (int)(threadIdx.x % (BN / 8)) * 8;
-    float sw[8], bias[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int64_t n = n0 + c0 + e < p.N ? n0 + c0 + e : p.N - 1;
-        sw[e] = p.w_scale[n];
-        bias[e] = p.bias ? p.bias[n] : 0.0f;
-    }
-    tile.store(smem, [&](int r, int c, const int (&v)[8]) {
-        if (r >= m_left || c >= n_left) return;
-        const int64_t m = m0 + r;
-        const float sa = p.a_scale[m];
-        float x[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = scaled(v[e], sa, sw[e], p.bias ? &bias[e] : nullptr);
-        const uint32_t at = (uint32_t)(n0 + c), cols = (uint32_t)p.N;
-        void *const to = row_of(p.D, m, p.ldd, p.out_f32 ? 4 : 2);
-        if (p.wide_out) {
-            if (p.out_f32) store8<true, true>(to, at, cols, x);
-            else store8<false, true>(to, at, cols, x);
-        } else {
-            if (p.out_f32) store8<true, false>(to, at, cols, x);
-            else store8<false, false>(to, at, cols, x);
-        }
-    });
+    if (p.out_f32) store_tile<true>(p, tile, smem, m0, m_left, n0, n_left);
+    else store_tile<false>(p, tile, smem, m0, m_left, n0, n_left);
 }
 
 // Few rows: NB * 16 channels and up to MB * 16 rows per workgroup.  The

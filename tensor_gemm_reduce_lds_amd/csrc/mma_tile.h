@@ -402,12 +402,14 @@ struct Tile {
         }
     }
 
-    // Hands the tile out as f(row, column, v[8]) for runs of 8 columns, each run
-    // once, whole rows by neighbouring lanes.  Accumulators pass through LDS one 32-row block
+    // Hands the tile out as f(row, c0, c1, v[8]): columns c0..c0 + 3 and c1..c1 + 3
+    // of a row, every column once, whole rows by neighbouring lanes.  c1 is c0 + 4,
+    // or with SPLIT (for 32-bit outputs) c0 + BN / 2, so that one 16-byte store of
+    // the lanes of a row covers a run of it either way.  Accumulators pass through LDS one 32-row block
     // row of every wave at a time: the direct layout would store 8 bytes per
     // row and instruction.  16-byte chunk c of a staged row r sits at
     // c ^ (r % 16).
-    template <class F>
+    template <bool SPLIT, class F>
     __device__ __forceinline__ void store(lds_t *smem, F f) const {
         constexpr int SROWS = WGM * 32, ROW = BN * 4, SBYTES = SROWS * ROW;
         constexpr bool TWICE = 2 * SBYTES <= LDS_BYTES;   // alternate between two halves
@@ -442,11 +444,12 @@ struct Tile {
             constexpr int LPR = BN / 8;
 #pragma unroll
             for (int u = 0; u < SROWS * LPR; u += THREADS) {
-                const int rr = (u + tid) / LPR, c = (tid % LPR) * 2;
+                const int rr = (u + tid) / LPR;
+                const int c = SPLIT ? tid % LPR : (tid % LPR) * 2, d = SPLIT ? c + LPR : c + 1;
                 const i32x4_t lo = *(lds_i32x4 *)(s + rr * ROW + ((c ^ (rr & 15)) << 4));
-                const i32x4_t hi = *(lds_i32x4 *)(s + rr * ROW + (((c + 1) ^ (rr & 15)) << 4));
+                const i32x4_t hi = *(lds_i32x4 *)(s + rr * ROW + ((d ^ (rr & 15)) << 4));
                 const int v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                f((rr >> 5) * WM + i * 32 + (rr & 31), (tid % LPR) * 8, v);
+                f((rr >> 5) * WM + i * 32 + (rr & 31), c * 4, d * 4, v);
             }
         }
     }

@@ -125,7 +125,7 @@ MANY = [90, 0, 141, 80] * 10
 
 @pytest.mark.parametrize("op", list(OPS))
 @pytest.mark.parametrize("sizes,N,K", [(MANY, 520, 72), (MANY, 776, 136), (MANY, 1032, 72), (MANY, 1032, 1032), ([3300, 1, 2900], 2056, 520),
-                                       ([1100, 0, 37, 900], 264, 72), ([5000], 264, 136), ([700, 0, 301], 257, 131)],
+                                       ([1100, 0, 37, 900], 264, 72), ([5000], 264, 136), ([700, 0, 301], 257, 131), ([450] * 8, 1288, 1288)],
                          ids=lambda v: str(sum(v)) if isinstance(v, list) else str(v))
 def test_every_tile(op, sizes, N, K):
     """Numbers of tiles from a few to several rounds, so that each tile of the
