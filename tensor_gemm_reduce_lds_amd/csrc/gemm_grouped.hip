@@ -604,15 +604,19 @@ hipError_t launch_rows(GroupedArgs &a, hipStream_t s) {
     }
 }
 
-// TN: 256 x 256 tiles, or 128 x 128 with two workgroups per CU, so that one
-// stores while the other loads: better for short groups, whose time is the
-// stores (us for 256 / 128: 190 rows per expert, 17 experts of 3136 x 1408 in 32
-// bits 84 / 73; 2048 rows, 8 experts of 4096 x 3584 422 / 565), and where there
-// are fewer large tiles than CUs.  With few of the small ones too, `parts`
-// workgroups share a tile's rows and a second kernel adds them, as many as take
-// the least time, from about 0.5 us per step of 64 rows, and for the second
-// kernel 4 us and the parts' traffic (16030 rows, 1296 x 304, 2 experts: 1 part 76
-// us, 4 38, 8 32; 7984 rows, 768 x 512, 8 experts: 1 part 20 us, 2 26).
+// TN: 256 x 256 tiles, which read the rows half as often, or 128 x 128 with two
+// workgroups per CU, so that one stores while the other loads.  With four rounds
+// of large tiles or more these are as fast where the caches hold the rows and
+// faster where they do not, as behind other work (us after a pass over 1 GB, for
+// 256 / 128: 6001 rows, 32 experts of 2048 x 1792 in 32 bits 136 / 165, 8000 rows,
+// 64 experts of 4096 x 1792 in bfloat16 321 / 404); with fewer rounds the small
+// ones lose less in the last (1992 rows, 9 experts of 1920 x 1840 in 32 bits 44 /
+// 40 without that pass), unless groups are long (2048 rows, 8 experts of 4096 x
+// 3584 422 / 565).  With few of the small ones too, `parts` workgroups share a
+// tile's rows and a second kernel adds them, as many as take the least time,
+// from about 0.5 us per step of 64 rows, and for the second kernel 4 us and the
+// parts' traffic (16030 rows, 1296 x 304, 2 experts: 1 part 76 us, 4 38, 8 32; 7984
+// rows, 768 x 512, 8 experts: 1 part 20 us, 2 26).
 struct TnChoice {
     bool large;
     int parts;
@@ -620,7 +624,7 @@ struct TnChoice {
 TnChoice tn_choice(int64_t rows, int64_t K, int64_t N, int64_t E) {
     const int64_t large = E * ((K + 255) / 256) * ((N + 255) / 256);
     const int64_t small = E * ((K + 127) / 128) * ((N + 127) / 128);
-    if (large >= kCus && rows / E >= 448) return {true, 1};
+    if (large >= 4 * kCus || (large >= kCus && rows / E >= 448)) return {true, 1};
     const double steps = (double)(rows / E) / 64, part_us = (double)E * K * N * 8 / 6.0e6;
     int parts = 1;
     double best_us = 0.5 * steps;
