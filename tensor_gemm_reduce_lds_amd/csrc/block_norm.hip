@@ -89,7 +89,7 @@ __device__ __forceinline__ const void *gate_at(const NormArgs &a, int64_t gate_r
 template <bool WIDE, int EPT, int THREADS, bool SF, bool YF, bool QUANT>
 __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
     constexpr int VPT = EPT / 8;
-    __shared__ float slots[2 * 16];
+    __shared__ JoinSlots<1> slots;
     int turn = 0;
     const int tid = threadIdx.x;
     const float inv_cols = 1.0f / (float)a.cols;
@@ -219,7 +219,7 @@ template <bool WIDE, int EPT, int THREADS, bool SF, bool YF, bool AHEAD>
 __global__ __launch_bounds__(THREADS) void norm_backward_kernel(NormArgs a) {
     constexpr int VPT = EPT / 8;
     using Row = BackwardRow<VPT, SF, YF>;
-    __shared__ float slots[2 * 3 * 16];
+    __shared__ JoinSlots<3> slots;
     int turn = 0;
     const int tid = threadIdx.x;
     const float inv_cols = 1.0f / (float)a.cols;

@@ -9,6 +9,7 @@
 #include <type_traits>
 
 #include "gemm_rs.h"
+#include "join_slots.h"
 
 namespace gemm_rs {
 namespace ffn {
@@ -217,27 +218,29 @@ __device__ __forceinline__ float wave_join(float v) {
 }
 
 // Join of NV values over a workgroup, in every thread; the order is fixed.
-// `slots` is the workgroup's [2][NV * 16] floats; `turn` alternates between
-// its halves, so one barrier per call is enough: a wave can write the half
-// that call n used only in call n+2, after the barrier of call n+1, which
-// every wave reaches after its reads of call n.
-template <class OP, int THREADS, int NV>
-__device__ __forceinline__ void block_join(float (&v)[NV], float *slots, int &turn) {
+// `turn` alternates between the halves of `slots`, which all joins of a kernel
+// share, so one barrier per call is enough.  A wave that has not finished the
+// reads of call n holds the others before the barrier of call n+1; until then
+// they write call n+1's half only, which no slot of call n lies in (whatever
+// the two NV are), and call n's half again in call n+2, behind that barrier.
+template <class OP, int THREADS, int NV, int MOST>
+__device__ __forceinline__ void block_join(float (&v)[NV], JoinSlots<MOST> &slots, int &turn) {
     constexpr int NW = THREADS / 64;
+    static_assert(NV <= MOST && NW <= JoinSlots<MOST>::kWaves, "a half holds a join");
 #pragma unroll
     for (int n = 0; n < NV; ++n) v[n] = wave_join<OP>(v[n]);
     if constexpr (NW > 1) {
-        float *s = slots + (turn & 1) * (NV * 16);
+        const int now = turn;
         turn ^= 1;
         if ((threadIdx.x & 63) == 0)
 #pragma unroll
-            for (int n = 0; n < NV; ++n) s[n * 16 + (threadIdx.x >> 6)] = v[n];
+            for (int n = 0; n < NV; ++n) slots.v[slots.at(now, n, threadIdx.x >> 6)] = v[n];
         lds_only_barrier();
 #pragma unroll
         for (int n = 0; n < NV; ++n) {
-            float t = s[n * 16];
+            float t = slots.v[slots.at(now, n, 0)];
 #pragma unroll
-            for (int w = 1; w < NW; ++w) t = OP::join(t, s[n * 16 + w]);
+            for (int w = 1; w < NW; ++w) t = OP::join(t, slots.v[slots.at(now, n, w)]);
             v[n] = t;
         }
     }

@@ -211,7 +211,7 @@ template <bool F32, bool WIDE, int EPT, int THREADS>
 __global__ __launch_bounds__(THREADS) void quantize_kernel(const void *x, int64_t rows, uint32_t cols,
                                                            int64_t ldx, int8_t *q, int64_t ldq,
                                                            float *scale) {
-    __shared__ float slots[2 * 16];
+    __shared__ JoinSlots<1> slots;
     int turn = 0;
     const uint32_t padded = (cols + 15) / 16 * 16, t0 = threadIdx.x * 8;
     constexpr int VPT = EPT ? EPT / 8 : 1;
