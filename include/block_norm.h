@@ -108,6 +108,8 @@ GEMM_RS_API int block_norm_plan(const block_norm_desc_t *desc, block_norm_plan_t
  *   u_scale [rows] floats (quant; NULL without): u ~ u_int8 * u_scale, with
  *           u_scale = max|u| / 127, and NaN for a row with a NaN or infinity
  * Other than x_out = x, no output may overlap an input or another output.
+ * With rows == 0 nothing is enqueued, and every array of rows (gate among
+ * them) may be NULL, as arrays without elements are.
  * Returns OK, INVALID_ARG (a missing or superfluous pointer, an address not
  * aligned to its element, rows out of range, another device) or HIP.
  */
@@ -125,8 +127,9 @@ GEMM_RS_API int block_norm_run(block_norm_plan_t plan, const void *x, const void
  *   dw_post, dw_pre   [cols] floats;  dgate [gate rows][cols] floats, of
  *           which a call writes those of its rows
  * The gradients of parameters are written, not added to; with rows == 0
- * dw_post and dw_pre are zeros and dgate has no rows.  No output may overlap
- * an input or another output.
+ * dw_post and dw_pre are zeros, dgate has no rows, and every pointer but
+ * w_post, w_pre, dw_post and dw_pre may be NULL.  No output may overlap an
+ * input or another output.
  * One plan's backward must not run on two streams at once (its workspace).
  */
 GEMM_RS_API int block_norm_backward(block_norm_plan_t plan, const void *dx_out, const void *du,

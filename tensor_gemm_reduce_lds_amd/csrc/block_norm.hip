@@ -595,6 +595,11 @@ NormArgs args_of(const block_norm_desc_t &d, int64_t rows) {
 bool fits(const void *p, bool wanted, size_t elem) {
     return wanted ? (p && aligned(p, elem)) : !p;
 }
+// The same of an array of rows, which a call without rows may leave out: an
+// array without elements need not have an address.
+bool fits_rows(const void *p, bool wanted, size_t elem, int64_t rows) {
+    return fits(p, wanted && (p || rows > 0), elem);
+}
 
 // Whether rows at p, ld elements apart, can be accessed 8 elements (8
 // bytes of int8) at a time.
@@ -638,9 +643,10 @@ int block_norm_run(block_norm_plan_t p, const void *x, const void *y, const void
     if (rows < 0 || rows > d.rows) return GEMM_RS_ERR_INVALID_ARG;
     const size_t se = type_bytes(d.stream_dtype), ye = type_bytes(d.dtype), pe = type_bytes(d.param_dtype);
     const size_t ue = d.quant ? 1 : ye;
-    if (!fits(x, true, se) || !fits(y, d.has_y, ye) || !fits(w_post, d.post, pe) ||
-        !fits(gate, d.rows_per_gate > 0, pe) || !fits(w_pre, d.pre, pe) ||
-        !fits(x_out, d.has_y, se) || !fits(u, d.pre, ue) || !fits(u_scale, d.quant, 4))
+    if (!fits_rows(x, true, se, rows) || !fits_rows(y, d.has_y, ye, rows) || !fits(w_post, d.post, pe) ||
+        !fits_rows(gate, d.rows_per_gate > 0, pe, rows) || !fits(w_pre, d.pre, pe) ||
+        !fits_rows(x_out, d.has_y, se, rows) || !fits_rows(u, d.pre, ue, rows) ||
+        !fits_rows(u_scale, d.quant, 4, rows))
         return GEMM_RS_ERR_INVALID_ARG;
     if (rows == 0) return GEMM_RS_OK;
     NormArgs a = args_of(d, rows);
@@ -675,10 +681,11 @@ int block_norm_backward(block_norm_plan_t p, const void *dx_out, const void *du,
     if (rows < 0 || rows > d.rows) return GEMM_RS_ERR_INVALID_ARG;
     const size_t se = type_bytes(d.stream_dtype), ye = type_bytes(d.dtype), pe = type_bytes(d.param_dtype);
     const bool gated = d.rows_per_gate > 0;
-    if (!fits(dx_out, dx_out || !d.pre, se) || !fits(du, d.pre, ye) || !fits(x_out, d.pre, se) ||
-        !fits(y, d.has_y, ye) || !fits(w_post, d.post, pe) || !fits(gate, gated, pe) ||
-        !fits(w_pre, d.pre, pe) || !fits(dx, true, se) || !fits(dy, d.has_y, ye) ||
-        !fits(dw_post, d.post, 4) || !fits(dgate, gated, 4) || !fits(dw_pre, d.pre, 4))
+    if (!fits_rows(dx_out, dx_out || !d.pre, se, rows) || !fits_rows(du, d.pre, ye, rows) ||
+        !fits_rows(x_out, d.pre, se, rows) || !fits_rows(y, d.has_y, ye, rows) || !fits(w_post, d.post, pe) ||
+        !fits_rows(gate, gated, pe, rows) || !fits(w_pre, d.pre, pe) || !fits_rows(dx, true, se, rows) ||
+        !fits_rows(dy, d.has_y, ye, rows) || !fits(dw_post, d.post, 4) || !fits_rows(dgate, gated, 4, rows) ||
+        !fits(dw_pre, d.pre, 4))
         return GEMM_RS_ERR_INVALID_ARG;
     hipStream_t s = (hipStream_t)stream;
     if (rows == 0) {

@@ -1,0 +1,58 @@
+"""Calls without rows, with tensors that have none (torch gives those no
+address): a rank or an expert layer that received no token makes them."""
+import pytest
+import torch
+
+from tensor_gemm_reduce_lds_amd import ffn as F
+from tensor_gemm_reduce_lds_amd import gemm_rs as G
+
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+BF, NAN = torch.bfloat16, float("nan")
+
+
+def _empty(cols, dtype=BF):
+    t = torch.empty((0, cols), dtype=dtype, device="cuda")
+    assert t.data_ptr() == 0
+    return t
+
+
+@pytest.mark.parametrize("quant", [0, 1])
+@pytest.mark.parametrize("rpg", [0, 4])
+def test_norm_forward(quant, rpg):
+    say("norm without rows", quant, rpg)
+    w = torch.ones(64, device="cuda")
+    e, gate = _empty(64), _empty(64, torch.float32) if rpg else None
+    u, us = (_empty(64, torch.int8), torch.empty(0, device="cuda")) if quant else (e, None)
+    s = torch.cuda.current_stream()
+    with F.BlockNormPlan(8, 64, rows_per_gate=rpg, quant=quant) as plan:
+        plan.run(e, e, w, gate, w, e, u, us, rows=0, stream=s)
+        # what has elements is still wanted, what the plan has not is still refused
+        for bad in ([(e, e, None, gate, w, e, u, us)] + ([] if quant else [(e, e, w, gate, w, e, u, w)])):
+            with pytest.raises(G.GemmRsError):
+                plan.run(*bad, rows=0, stream=s)
+        with pytest.raises(G.GemmRsError):
+            plan.run(e, e, w, gate, w, e, u, us, rows=1, stream=s)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("rpg", [0, 4])
+def test_norm_backward_zeroes_the_weights_gradients(rpg):
+    say("norm backward without rows", rpg)
+    w, dw = torch.ones(64, device="cuda"), torch.full((2, 64), NAN, device="cuda")
+    e, g = _empty(64), _empty(64, torch.float32) if rpg else None
+    s = torch.cuda.current_stream()
+    with F.BlockNormPlan(8, 64, rows_per_gate=rpg, backward=1) as plan:
+        for i, dxo in enumerate((e, None)):
+            dw.fill_(NAN)
+            plan.backward(dxo, e, e, e, w, g, w, e, e, dw[0], g, dw[1], rows=0, stream=s)
+            torch.cuda.synchronize()
+            assert not dw.any() and not dw.isnan().any()
+        for a, b in ((None, dw[1]), (dw[0], None)):
+            with pytest.raises(G.GemmRsError):
+                plan.backward(e, e, e, e, w, g, w, e, e, a, g, b, rows=0, stream=s)
+        with pytest.raises(G.GemmRsError):
+            plan.backward(e, e, e, e, w, g, w, e, e, dw[0], g, dw[1], rows=1, stream=s)
+    torch.cuda.synchronize()
