@@ -73,6 +73,8 @@ GEMM_RS_API int gemm_q8_plan(const gemm_q8_desc_t *desc, gemm_q8_plan_t *out);
  *   bias    float [N], NULL without has_bias
  *   D       [rows][ldd] of out_dtype, element-aligned; it may not overlap
  *           an input
+ * With rows == 0 nothing is enqueued, and a, a_scale and D may be NULL, as
+ * arrays without elements are.
  * Returns OK, INVALID_ARG (missing, superfluous or misaligned pointers, rows
  * out of range, another device) or HIP.
  */
@@ -84,10 +86,11 @@ GEMM_RS_API int gemm_q8_run(gemm_q8_plan_t plan, const void *a, const void *a_sc
  * gemm_q8_quantize: rows x cols of `dtype` (row stride ldx elements) to int8
  * rows of stride ldq bytes and one float scale per row; columns
  * cols..ceil(cols/16)*16 of the output are zeros (ldq holds them).  Enqueued
- * on `stream`.  rows may be 0; q and scale may not overlap x.  Returns OK, INVALID_ARG (NULL or misaligned
- * pointers: x to its element; rows < 0, cols < 1, ldx < cols, ldq below
- * ceil(cols/16)*16, unknown type), UNSUPPORTED (cols of 2^17 or more, rows
- * or strides of 2^31 or more) or HIP.
+ * on `stream`.  rows may be 0, and x, q and scale NULL then; q and scale may
+ * not overlap x.  Returns OK, INVALID_ARG (NULL or misaligned pointers: x to
+ * its element; rows < 0, cols < 1, ldx < cols, ldq below ceil(cols/16)*16,
+ * unknown type), UNSUPPORTED (cols of 2^17 or more, rows or strides of 2^31 or
+ * more) or HIP.
  */
 GEMM_RS_API int gemm_q8_quantize(const void *x, int32_t dtype, int64_t rows, int64_t cols,
                                  int64_t ldx, void *q, int64_t ldq, void *scale, void *stream);

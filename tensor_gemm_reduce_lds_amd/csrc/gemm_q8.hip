@@ -360,7 +360,8 @@ int gemm_q8_run(gemm_q8_plan_t p, const void *a, const void *a_scale, const void
     if (!p || !on_device(p->device)) return GEMM_RS_ERR_INVALID_ARG;
     const gemm_q8_desc_t &d = p->d;
     if (rows < 0 || rows > d.M) return GEMM_RS_ERR_INVALID_ARG;
-    if (!a || !a_scale || !w || !w_scale || !D || (bias != nullptr) != (d.has_bias != 0))
+    // (arrays of no rows need not have an address)
+    if ((rows > 0 && (!a || !a_scale || !D)) || !w || !w_scale || (bias != nullptr) != (d.has_bias != 0))
         return GEMM_RS_ERR_INVALID_ARG;
     if (!aligned(a, 16) || !aligned(w, 16) || !aligned(a_scale, 4) || !aligned(w_scale, 4) ||
         !aligned(bias, 4) || !aligned(D, type_bytes(d.out_dtype)))
@@ -388,7 +389,7 @@ int gemm_q8_quantize(const void *x, int32_t dtype, int64_t rows, int64_t cols, i
                      int64_t ldq, void *scale, void *stream) {
     if (!known_type(dtype) || rows < 0 || cols < 1 || ldx < cols || ldq < (cols + 15) / 16 * 16)
         return GEMM_RS_ERR_INVALID_ARG;
-    if (!x || !q || !scale || !aligned(x, type_bytes(dtype)) || !aligned(scale, 4))
+    if ((rows > 0 && (!x || !q || !scale)) || !aligned(x, type_bytes(dtype)) || !aligned(scale, 4))
         return GEMM_RS_ERR_INVALID_ARG;
     if (cols >= kMaxK || rows > INT32_MAX || ldx > INT32_MAX || ldq > INT32_MAX)
         return GEMM_RS_ERR_UNSUPPORTED;

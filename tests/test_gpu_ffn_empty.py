@@ -56,3 +56,21 @@ def test_norm_backward_zeroes_the_weights_gradients(rpg):
         with pytest.raises(G.GemmRsError):
             plan.backward(e, e, e, e, w, g, w, e, e, dw[0], g, dw[1], rows=1, stream=s)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("bias", [0, 1])
+def test_q8(bias):
+    say("q8 without rows", bias)
+    q, sq, x, y = _empty(64, torch.int8), torch.empty(0, device="cuda"), _empty(64), _empty(32)
+    w, sw = torch.zeros((32, 64), dtype=torch.int8, device="cuda"), torch.ones(32, device="cuda")
+    s = torch.cuda.current_stream()
+    F.q8_quantize(x, q, sq, 0, 64, stream=s)
+    with F.Q8Plan(8, 32, 64, has_bias=bias) as plan:
+        b = sw if bias else None
+        plan.run(q, sq, w, sw, b, y, rows=0, stream=s)
+        for bad in ((None, sw, b), (w, None, b), (w, sw, None if bias else sw)):
+            with pytest.raises(G.GemmRsError):
+                plan.run(q, sq, *bad, y, rows=0, stream=s)
+        with pytest.raises(G.GemmRsError):
+            plan.run(q, sq, w, sw, b, y, rows=1, stream=s)
+    torch.cuda.synchronize()
