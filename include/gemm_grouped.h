@@ -86,6 +86,9 @@ GEMM_RS_API int gemm_grouped_plan(const gemm_grouped_desc_t *desc, gemm_grouped_
  *            Other values are clipped to that (no access leaves the
  *            arrays) and reported by gemm_grouped_status.
  *   C        may not overlap an input
+ * With rows == 0 NN and NT enqueue nothing (and look at no offsets), TN writes
+ * zeros (with `accumulate` nothing); arrays of rows (A, C of NN and NT, B of TN)
+ * may be NULL then, as arrays without elements are.
  * One plan of TN must not run on two streams at once (its workspace).
  * Returns OK, INVALID_ARG (NULL or misaligned pointers, rows out of range,
  * another device) or HIP.

@@ -748,10 +748,12 @@ int gemm_grouped_run(gemm_grouped_plan_t p, const void *A, const void *B, const 
     if (!p || !on_device(p->device)) return GEMM_RS_ERR_INVALID_ARG;
     const gemm_grouped_desc_t &d = p->d;
     if (rows < 0 || rows > d.M) return GEMM_RS_ERR_INVALID_ARG;
-    if (!A || !B || !offsets || !C || !aligned(A, 2) || !aligned(B, 2) || !aligned(offsets, 4) ||
-        !aligned(C, type_bytes(d.out_dtype)))
+    // arrays of no rows (A, and C or TN's B) need not have an address
+    const bool tn = d.op == GEMM_GROUPED_TN, some = rows > 0;
+    if ((!A && some) || (!B && (some || !tn)) || (!C && (some || tn)) || !offsets || !aligned(A, 2) ||
+        !aligned(B, 2) || !aligned(offsets, 4) || !aligned(C, type_bytes(d.out_dtype)))
         return GEMM_RS_ERR_INVALID_ARG;
-    if (rows == 0 && d.op != GEMM_GROUPED_TN) return GEMM_RS_OK;
+    if (rows == 0 && !tn) return GEMM_RS_OK;
     GroupedArgs a = {};
     a.rows = rows;
     a.N = d.N;

@@ -74,3 +74,28 @@ def test_q8(bias):
         with pytest.raises(G.GemmRsError):
             plan.run(q, sq, w, sw, b, y, rows=1, stream=s)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("op", [F.GROUPED_NN, F.GROUPED_NT, F.GROUPED_TN])
+@pytest.mark.parametrize("N,K", [(64, 128), (33, 7)])
+def test_grouped(op, N, K):
+    """No rows at all: NN and NT have nothing to write, the weight gradient is
+    zeros, or what it was with `accumulate`."""
+    say("grouped without rows", op, N, K)
+    tn = op == F.GROUPED_TN
+    a = _empty(K)
+    b = _empty(N) if tn else torch.ones((3, K, N), dtype=BF, device="cuda")
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    s = torch.cuda.current_stream()
+    for accumulate in ((0, 1) if tn else (0,)):
+        with F.GroupedPlan(10, N, K, 3, op, accumulate=accumulate) as plan:
+            c = torch.full((3, K, N), 7.0, dtype=BF, device="cuda") if tn else _empty(N)
+            plan.run(a, b, off, c, rows=0, stream=s)
+            assert plan.status(s)[0] == G.OK
+            assert not tn or bool((c == (7.0 if accumulate else 0.0)).all())
+            for bad in ((a, b, None, c), (a, b, off, None) if tn else (a, None, off, c)):
+                with pytest.raises(G.GemmRsError):
+                    plan.run(*bad, rows=0, stream=s)
+            with pytest.raises(G.GemmRsError):
+                plan.run(a, b, off, c, rows=1, stream=s)
+            assert plan.status(s)[0] == G.OK
