@@ -131,6 +131,14 @@ def _addresses(*tensors):
     return [t if t is None or t.__class__ is int else t.data_ptr() for t in tensors]
 
 
+def _check_offsets(t, n):
+    """Refuses a tensor that does not hold n int32 one after another on the GPU:
+    the kernels would take its bits for offsets, and most would pass for valid
+    ones (int64, the default of cumsum, reads as 0 every other time)."""
+    if t.element_size() != 4 or t.is_floating_point() or t.numel() < n or not (t.is_cuda and t.is_contiguous()):
+        raise GemmRsError(ERR_INVALID_ARG, "gemm_grouped_run: offsets are not %d contiguous int32 on the GPU" % n)
+
+
 class _Plan:
     """Owns one plan handle of the family `_name`."""
 
@@ -238,8 +246,12 @@ class GroupedPlan(_Plan):
         super().__init__(gemm_grouped_desc_t(M=M, N=N, K=K, E=E, op=op, out_dtype=out_dtype,
                                              accumulate=accumulate, lda=lda, ldb=ldb, ldc=ldc))
         self._rows = M
+        self._offsets = E + 1
 
     def run(self, A, B, offsets, C, rows=None, stream=None):
+        """offsets: an int32 tensor of E + 1 on the GPU, or an address."""
+        if offsets is not None and offsets.__class__ is not int:
+            _check_offsets(offsets, self._offsets)
         rc = self._run(self.handle, *_addresses(A, B, offsets, C),
                        self._rows if rows is None else rows, _stream_handle(stream))
         if rc != OK:
