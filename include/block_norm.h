@@ -12,8 +12,8 @@
  *     u  = x' * r1 * (o + w_pre),    r1 = 1/sqrt(mean(x'*x') + eps_pre)
  *
  * x' is the new residual stream, u the next block's input.  u can be
- * written as 8-bit integers with one scale per row (the input of
- * gemm_q8.h).  Sums and statistics are 32-bit floats; u is computed from
+ * written as 8-bit integers with one scale per row (the input of gemm_q8.h,
+ * whose rows are padded with zeros to a multiple of 16).  Sums and statistics are 32-bit floats; u is computed from
  * the unrounded x'.
  *
  * Backward, from dx' (gradient of the stream after this point) and du:
@@ -104,7 +104,8 @@ GEMM_RS_API int block_norm_plan(const block_norm_desc_t *desc, block_norm_plan_t
  *   x       [rows][ld_x];  x_out [rows][ld_x_out] (has_y; NULL without; may
  *           be x itself if the strides agree)
  *   y, w_post, gate, w_pre   as the descriptor has them, NULL where it has not
- *   u       [rows][ld_u] (pre; NULL without): dtype, or int8 with quant
+ *   u       [rows][ld_u] (pre; NULL without): dtype, or int8 with quant, where
+ *           columns cols..ceil(cols/16)*16 are zeros if ld_u holds them
  *   u_scale [rows] floats (quant; NULL without): u ~ u_int8 * u_scale, with
  *           u_scale = max|u| / 127, and NaN for a row with a NaN or infinity
  * Other than x_out = x, no output may overlap an input or another output.

@@ -35,8 +35,9 @@ extern "C" {
 /*
  * Problem descriptor.
  *   M          most rows (tokens) of a call; N channels; K contraction,
- *              a multiple of 16 below 2^17 (pad rows with zeros up to it:
- *              gemm_q8_quantize does)
+ *              a multiple of 16 below 2^17 (pad the rows of a or of w with
+ *              zeros up to it: gemm_q8_quantize does, and the block norm's
+ *              int8 output does where its row stride has the room)
  *   lda, ldw   row strides in bytes, multiples of 16, 0: K
  *   ldd        row stride of D in elements, 0: N
  *   out_dtype  GEMM_RS_BF16 or GEMM_RS_F32

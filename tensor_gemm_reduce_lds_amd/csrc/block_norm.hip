@@ -35,6 +35,7 @@ struct NormArgs {
     const void *x, *y, *w_post, *gate, *w_pre;
     void *x_out, *u;
     float *u_scale;
+    int64_t q_cols;       // columns of int8 rows that are written: zeros past cols
     const void *dx_out, *du;
     void *dx, *dy;
     float *dgate;
@@ -168,11 +169,12 @@ __global__ __launch_bounds__(THREADS) void norm_forward_kernel(NormArgs a) {
             block_join<MaxBits, THREADS, 1>(m, slots, turn);
             const QuantRow q = quant_row(m[0]);
             if (tid == 0) a.u_scale[row] = q.scale;
+            const uint32_t q_cols = (uint32_t)a.q_cols;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) {
                 const uint32_t c = (uint32_t)(k * THREADS + tid) * 8;
-                if (c >= cols) continue;
-                quant8<WIDE>(q, (int8_t *)row_of(a.u, row, a.ld_u, 1), c, cols,
+                if (c >= q_cols) continue;
+                quant8<WIDE>(q, (int8_t *)row_of(a.u, row, a.ld_u, 1), c, q_cols,
                              [&](int e) { return x[k * 8 + e]; });
             }
         } else {
@@ -659,6 +661,9 @@ int block_norm_run(block_norm_plan_t p, const void *x, const void *y, const void
     a.x_out = x_out;
     a.u = u;
     a.u_scale = (float *)u_scale;
+    // (a kernel shape holds whole runs of 16 columns, so these too)
+    const int64_t padded = (d.cols + 15) / 16 * 16;
+    a.q_cols = a.ld_u >= padded ? padded : d.cols;
     const bool wide_rows = d.cols % 8 == 0 && wide(x, a.ld_x, se) && wide(y, a.ld_y, ye) &&
                      wide(w_post, 8, pe) && wide(gate, 8, pe) && wide(w_pre, 8, pe) &&
                      wide(x_out, a.ld_x_out, se) && wide(u, a.ld_u, ue);
