@@ -460,21 +460,18 @@ __global__ void norm_zero_kernel(float *a, float *b, int64_t n) {
 }
 
 template <bool WIDE, int EPT, int THREADS>
-void launch_forward(const NormArgs &a, bool sf, bool yf, bool quant, int64_t grid, hipStream_t s) {
-    auto go = [&](auto *kernel) {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(THREADS), 0, s, a);
-    };
+hipError_t launch_forward(const NormArgs &a, bool sf, bool yf, bool quant, int64_t grid, hipStream_t s) {
+    auto go = [&](auto *kernel) { return launch(kernel, dim3((unsigned)grid), THREADS, 0, s, a); };
     if (quant) {
-        if (sf && yf) go(norm_forward_kernel<WIDE, EPT, THREADS, true, true, true>);
-        else if (sf) go(norm_forward_kernel<WIDE, EPT, THREADS, true, false, true>);
-        else if (yf) go(norm_forward_kernel<WIDE, EPT, THREADS, false, true, true>);
-        else go(norm_forward_kernel<WIDE, EPT, THREADS, false, false, true>);
-    } else {
-        if (sf && yf) go(norm_forward_kernel<WIDE, EPT, THREADS, true, true, false>);
-        else if (sf) go(norm_forward_kernel<WIDE, EPT, THREADS, true, false, false>);
-        else if (yf) go(norm_forward_kernel<WIDE, EPT, THREADS, false, true, false>);
-        else go(norm_forward_kernel<WIDE, EPT, THREADS, false, false, false>);
+        if (sf && yf) return go(norm_forward_kernel<WIDE, EPT, THREADS, true, true, true>);
+        if (sf) return go(norm_forward_kernel<WIDE, EPT, THREADS, true, false, true>);
+        if (yf) return go(norm_forward_kernel<WIDE, EPT, THREADS, false, true, true>);
+        return go(norm_forward_kernel<WIDE, EPT, THREADS, false, false, true>);
     }
+    if (sf && yf) return go(norm_forward_kernel<WIDE, EPT, THREADS, true, true, false>);
+    if (sf) return go(norm_forward_kernel<WIDE, EPT, THREADS, true, false, false>);
+    if (yf) return go(norm_forward_kernel<WIDE, EPT, THREADS, false, true, false>);
+    return go(norm_forward_kernel<WIDE, EPT, THREADS, false, false, false>);
 }
 
 template <bool WIDE, int EPT, int THREADS>
@@ -621,14 +618,13 @@ int block_norm_plan(const block_norm_desc_t *desc, block_norm_plan_t *out) {
     block_norm_plan_s *p = (block_norm_plan_s *)calloc(1, sizeof(block_norm_plan_s));
     if (!p) return GEMM_RS_ERR_HIP;
     p->d = *desc;
-    if (hipGetDevice(&p->device) != hipSuccess) {
+    if (own(hipGetDevice(&p->device)) != hipSuccess) {
         free(p);
         return GEMM_RS_ERR_HIP;
     }
     if (desc->backward) {
         p->part_bytes = backward_wgs(desc->rows, desc->cols) * 4 * desc->cols * (int64_t)sizeof(float);
-        if (hipMalloc((void **)&p->part, p->part_bytes) != hipSuccess) {
-            (void)hipGetLastError();
+        if (own(hipMalloc((void **)&p->part, p->part_bytes)) != hipSuccess) {
             free(p);
             return GEMM_RS_ERR_HIP;
         }
@@ -667,14 +663,15 @@ int block_norm_run(block_norm_plan_t p, const void *x, const void *y, const void
     const bool wide_rows = d.cols % 8 == 0 && wide(x, a.ld_x, se) && wide(y, a.ld_y, ye) &&
                      wide(w_post, 8, pe) && wide(gate, 8, pe) && wide(w_pre, 8, pe) &&
                      wide(x_out, a.ld_x_out, se) && wide(u, a.ld_u, ue);
+    hipError_t e = hipSuccess;
     forward_shape(rows, d.cols, [&](auto sh) {
         using S = decltype(sh);
         const int64_t most = (int64_t)kCus * 2048 / S::THREADS, grid = rows < most ? rows : most;
         const bool sf = d.stream_dtype == GEMM_RS_F32, yf = d.dtype == GEMM_RS_F32;
-        if (wide_rows) launch_forward<true, S::EPT, S::THREADS>(a, sf, yf, d.quant != 0, grid, (hipStream_t)stream);
-        else launch_forward<false, S::EPT, S::THREADS>(a, sf, yf, d.quant != 0, grid, (hipStream_t)stream);
+        e = wide_rows ? launch_forward<true, S::EPT, S::THREADS>(a, sf, yf, d.quant != 0, grid, (hipStream_t)stream)
+                      : launch_forward<false, S::EPT, S::THREADS>(a, sf, yf, d.quant != 0, grid, (hipStream_t)stream);
     });
-    return hipGetLastError() == hipSuccess ? GEMM_RS_OK : GEMM_RS_ERR_HIP;
+    return e == hipSuccess ? GEMM_RS_OK : GEMM_RS_ERR_HIP;
 }
 
 int block_norm_backward(block_norm_plan_t p, const void *dx_out, const void *du, const void *x_out,
@@ -693,11 +690,12 @@ int block_norm_backward(block_norm_plan_t p, const void *dx_out, const void *du,
         !fits(dw_pre, d.pre, 4))
         return GEMM_RS_ERR_INVALID_ARG;
     hipStream_t s = (hipStream_t)stream;
+    hipError_t e = hipSuccess;
     if (rows == 0) {
         if (dw_post || dw_pre)
-            hipLaunchKernelGGL(norm_zero_kernel, dim3((unsigned)((d.cols + 255) / 256)), dim3(256), 0, s,
-                               (float *)dw_post, (float *)dw_pre, d.cols);
-        return hipGetLastError() == hipSuccess ? GEMM_RS_OK : GEMM_RS_ERR_HIP;
+            e = launch(norm_zero_kernel, dim3((unsigned)((d.cols + 255) / 256)), 256, 0, s, (float *)dw_post,
+                       (float *)dw_pre, d.cols);
+        return e == hipSuccess ? GEMM_RS_OK : GEMM_RS_ERR_HIP;
     }
     NormArgs a = args_of(d, rows);
     a.x_out = (void *)x_out;
@@ -718,7 +716,6 @@ int block_norm_backward(block_norm_plan_t p, const void *dx_out, const void *du,
     int64_t wgs = backward_wgs(rows, d.cols);
     a.rows_per_wg = (rows + wgs - 1) / wgs;
     wgs = (rows + a.rows_per_wg - 1) / a.rows_per_wg;
-    hipError_t e = hipSuccess;
     backward_shape(d.cols, [&](auto sh) {
         using S = decltype(sh);
         const bool sf = d.stream_dtype == GEMM_RS_F32, yf = d.dtype == GEMM_RS_F32;
@@ -732,10 +729,10 @@ int block_norm_backward(block_norm_plan_t p, const void *dx_out, const void *du,
         const int64_t gates = (rows + a.rows_per_gate - 1) / a.rows_per_gate;
         const bool by_group = gates < wgs - 1;
         const unsigned ny = 2 + (split ? (unsigned)(by_group ? gates : wgs - 1) : 0);
-        hipLaunchKernelGGL(norm_join_kernel, dim3((unsigned)((d.cols + 31) / 32), ny), dim3(1024), 0, s,
-                           a, wgs, (int)by_group, (float *)dw_post, (float *)dw_pre);
+        e = launch(norm_join_kernel, dim3((unsigned)((d.cols + 31) / 32), ny), 1024, 0, s, a, wgs, (int)by_group,
+                   (float *)dw_post, (float *)dw_pre);
     }
-    return hipGetLastError() == hipSuccess ? GEMM_RS_OK : GEMM_RS_ERR_HIP;
+    return e == hipSuccess ? GEMM_RS_OK : GEMM_RS_ERR_HIP;
 }
 
 int block_norm_query(block_norm_plan_t p, block_norm_info_t *info) {
@@ -750,11 +747,11 @@ int block_norm_destroy(block_norm_plan_t p) {
     if (!p) return GEMM_RS_OK;
     int cur = -1;
     bool switched = false;
-    if (p->part && hipGetDevice(&cur) == hipSuccess && cur != p->device)
-        switched = hipSetDevice(p->device) == hipSuccess;
+    if (p->part && own(hipGetDevice(&cur)) == hipSuccess && cur != p->device)
+        switched = own(hipSetDevice(p->device)) == hipSuccess;
     // teardown is best effort: a failure here leaves nothing to undo
-    if (p->part) (void)hipFree(p->part);
-    if (switched) (void)hipSetDevice(cur);
+    if (p->part) (void)own(hipFree(p->part));
+    if (switched) (void)own(hipSetDevice(cur));
     free(p);
     return GEMM_RS_OK;
 }

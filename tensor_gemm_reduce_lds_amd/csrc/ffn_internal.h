@@ -16,10 +16,18 @@ namespace ffn {
 
 constexpr int kCus = 256;   // MI355X: 8 XCDs x 32 CUs
 
+// The result of a HIP call.  An error is returned and not left behind as the
+// thread's last one, which a later call, also of another library, would report
+// as its own.
+inline hipError_t own(hipError_t e) {
+    if (e != hipSuccess) (void)hipGetLastError();
+    return e;
+}
+
 // work is only enqueued while the plan's device is current
 inline bool on_device(int device) {
     int cur = -1;
-    return hipGetDevice(&cur) == hipSuccess && cur == device;
+    return own(hipGetDevice(&cur)) == hipSuccess && cur == device;
 }
 
 inline bool aligned(const void *p, size_t bytes) { return ((uintptr_t)p % bytes) == 0; }
@@ -282,23 +290,34 @@ __device__ __forceinline__ void quant8(const QuantRow &q, int8_t *row, uint32_t 
     }
 }
 
-// Launches a kernel with dynamic LDS, whose limit is a per-device attribute of
-// the kernel: set on the first launch there (threads that race set it twice).
+// Launches a kernel.  The result is this launch's: the thread's last error may
+// be an older one of the caller's, who may not have asked for it, and stays his.
+template <class... P, class... A>
+inline hipError_t launch(void (*kernel)(P...), dim3 grid, int threads, int lds_bytes, hipStream_t s, const A &...args) {
+    static_assert(sizeof...(P) == sizeof...(A), "an argument for each parameter");
+    return [&](P... held) {      // the arguments in the parameters' types
+        void *at[] = {(void *)&held...};
+        return own(hipLaunchKernel((const void *)kernel, grid, dim3((unsigned)threads), at, (size_t)lds_bytes, s));
+    }(args...);
+}
+
+// The same with dynamic LDS, whose limit is a per-device attribute of the
+// kernel: set on the first launch there (threads that race set it twice).
 template <auto KERNEL, class ARGS>
 inline hipError_t launch_lds(int64_t blocks, int threads, int lds_bytes, hipStream_t s, const ARGS &a) {
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> set[kMaxDevices];
     int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kMaxDevices)
-        return hipErrorInvalidDevice;
+    const hipError_t got = own(hipGetDevice(&dev));
+    if (got != hipSuccess) return got;
+    if (dev < 0 || dev >= kMaxDevices) return hipErrorInvalidDevice;
     if (!set[dev].load(std::memory_order_acquire)) {
-        const hipError_t e = hipFuncSetAttribute((const void *)KERNEL,
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, lds_bytes);
+        const hipError_t e = own(hipFuncSetAttribute((const void *)KERNEL,
+                                                     hipFuncAttributeMaxDynamicSharedMemorySize, lds_bytes));
         if (e != hipSuccess) return e;
         set[dev].store(true, std::memory_order_release);
     }
-    hipLaunchKernelGGL(KERNEL, dim3((unsigned)blocks), dim3(threads), lds_bytes, s, a);
-    return hipGetLastError();
+    return launch(KERNEL, dim3((unsigned)blocks), threads, lds_bytes, s, a);
 }
 
 }  // namespace ffn

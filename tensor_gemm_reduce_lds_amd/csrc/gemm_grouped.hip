@@ -656,8 +656,7 @@ hipError_t launch_tn(GroupedArgs &a, int max_parts, hipStream_t s) {
     hipError_t e = launch_tile<GEMM_GROUPED_TN, 128, 128, 2, 2, 2, 3>(a, s);
     if (e != hipSuccess || a.parts == 1) return e;
     const int64_t blocks = ((int64_t)a.E * a.K * (a.N / 8) + 255) / 256;
-    hipLaunchKernelGGL(grouped_join_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), dim3(256), 0, s, a);
-    return hipGetLastError();
+    return launch(grouped_join_kernel, dim3((unsigned)(blocks < 4096 ? blocks : 4096)), 256, 0, s, a);
 }
 
 template <int OP>
@@ -667,8 +666,7 @@ hipError_t launch_op(GroupedArgs &a, bool wide, int max_parts, hipStream_t s) {
         a.tiles_m = (int32_t)((a.K + 63) / 64);
         const int64_t row_tiles = OP == GEMM_GROUPED_TN ? (int64_t)a.E * a.tiles_m
                                                         : a.rows / 64 + (a.E < a.rows ? a.E : a.rows);
-        hipLaunchKernelGGL(grouped_narrow_kernel<OP>, dim3((unsigned)(row_tiles * a.tiles_n)), dim3(256), 0, s, a);
-        return hipGetLastError();
+        return launch(grouped_narrow_kernel<OP>, dim3((unsigned)(row_tiles * a.tiles_n)), 256, 0, s, a);
     }
     if constexpr (OP == GEMM_GROUPED_TN) return launch_tn(a, max_parts, s);
     else return launch_rows<OP>(a, s);
@@ -725,17 +723,17 @@ int gemm_grouped_plan(const gemm_grouped_desc_t *desc, gemm_grouped_plan_t *out)
     if (!p->d.lda) p->d.lda = p->d.K;
     if (!p->d.ldb) p->d.ldb = p->d.op == GEMM_GROUPED_NT ? p->d.K : p->d.N;
     if (!p->d.ldc) p->d.ldc = p->d.N;
-    hipError_t e = hipGetDevice(&p->device);
-    if (e == hipSuccess) e = hipMalloc((void **)&p->err, 16);
+    hipError_t e = own(hipGetDevice(&p->device));
+    if (e == hipSuccess) e = own(hipMalloc((void **)&p->err, 16));
     p->parts = most_parts(p->d);
     p->slot_bytes = p->parts > 1 ? p->parts * p->d.E * p->d.K * p->d.N * (int64_t)sizeof(float) : 0;
-    if (e == hipSuccess && p->slot_bytes) e = hipMalloc((void **)&p->slots, p->slot_bytes);
+    if (e == hipSuccess && p->slot_bytes) e = own(hipMalloc((void **)&p->slots, p->slot_bytes));
     // a blocking copy: the word is zero before any later launch on any stream
     const int32_t zero[4] = {0, 0, 0, 0};
-    if (e == hipSuccess) e = hipMemcpy(p->err, zero, 16, hipMemcpyHostToDevice);
+    if (e == hipSuccess) e = own(hipMemcpy(p->err, zero, 16, hipMemcpyHostToDevice));
     if (e != hipSuccess) {
-        if (p->err) (void)hipFree(p->err);
-        if (p->slots) (void)hipFree(p->slots);
+        if (p->err) (void)own(hipFree(p->err));
+        if (p->slots) (void)own(hipFree(p->slots));
         free(p);
         return GEMM_RS_ERR_HIP;
     }
@@ -784,10 +782,10 @@ int gemm_grouped_run(gemm_grouped_plan_t p, const void *A, const void *B, const 
 int gemm_grouped_status(gemm_grouped_plan_t p, void *stream, int32_t *detail) {
     if (!p || !on_device(p->device)) return GEMM_RS_ERR_INVALID_ARG;
     int32_t h[4] = {0, 0, 0, 0};
-    hipError_t e = hipStreamSynchronize((hipStream_t)stream);
-    if (e == hipSuccess) e = hipMemcpy(h, p->err, 16, hipMemcpyDeviceToHost);
+    hipError_t e = own(hipStreamSynchronize((hipStream_t)stream));
+    if (e == hipSuccess) e = own(hipMemcpy(h, p->err, 16, hipMemcpyDeviceToHost));
     const int32_t zero[4] = {0, 0, 0, 0};
-    if (e == hipSuccess && h[0] != 0) e = hipMemcpy(p->err, zero, 16, hipMemcpyHostToDevice);
+    if (e == hipSuccess && h[0] != 0) e = own(hipMemcpy(p->err, zero, 16, hipMemcpyHostToDevice));
     if (e != hipSuccess) return GEMM_RS_ERR_HIP;
     if (detail)
         for (int i = 0; i < 4; ++i) detail[i] = h[i];
@@ -804,12 +802,12 @@ int gemm_grouped_destroy(gemm_grouped_plan_t p) {
     if (!p) return GEMM_RS_OK;
     int cur = -1;
     bool switched = false;
-    if (hipGetDevice(&cur) == hipSuccess && cur != p->device)
-        switched = hipSetDevice(p->device) == hipSuccess;
+    if (own(hipGetDevice(&cur)) == hipSuccess && cur != p->device)
+        switched = own(hipSetDevice(p->device)) == hipSuccess;
     // teardown is best effort: a failure here leaves nothing to undo
-    (void)hipFree(p->err);
-    if (p->slots) (void)hipFree(p->slots);
-    if (switched) (void)hipSetDevice(cur);
+    (void)own(hipFree(p->err));
+    if (p->slots) (void)own(hipFree(p->slots));
+    if (switched) (void)own(hipSetDevice(cur));
     free(p);
     return GEMM_RS_OK;
 }

@@ -347,7 +347,7 @@ int gemm_q8_plan(const gemm_q8_desc_t *desc, gemm_q8_plan_t *out) {
     if (!p->d.lda) p->d.lda = p->d.K;
     if (!p->d.ldw) p->d.ldw = p->d.K;
     if (!p->d.ldd) p->d.ldd = p->d.N;
-    if (hipGetDevice(&p->device) != hipSuccess) {
+    if (own(hipGetDevice(&p->device)) != hipSuccess) {
         free(p);
         return GEMM_RS_ERR_HIP;
     }
@@ -396,9 +396,10 @@ int gemm_q8_quantize(const void *x, int32_t dtype, int64_t rows, int64_t cols, i
     if (rows == 0) return GEMM_RS_OK;
     const bool vec = cols % 8 == 0 && ldx % 8 == 0 && ldq % 8 == 0 && aligned(x, 16) && aligned(q, 8);
     const dim3 grid((unsigned)(rows < 65536 ? rows : 65536));
+    hipError_t e = hipSuccess;
     auto go = [&](auto *kernel, int threads) {
-        hipLaunchKernelGGL(kernel, grid, dim3(threads), 0, (hipStream_t)stream, x, rows, (uint32_t)cols, ldx,
-                           (int8_t *)q, ldq, (float *)scale);
+        e = launch(kernel, grid, threads, 0, (hipStream_t)stream, x, rows, (uint32_t)cols, ldx, (int8_t *)q, ldq,
+                   (float *)scale);
     };
     auto of_type = [&](auto f32, auto wide) {
         constexpr bool F = decltype(f32)::value, W = decltype(wide)::value;
@@ -411,7 +412,7 @@ int gemm_q8_quantize(const void *x, int32_t dtype, int64_t rows, int64_t cols, i
     };
     if (dtype == GEMM_RS_F32) vec ? of_type(std::true_type{}, std::true_type{}) : of_type(std::true_type{}, std::false_type{});
     else vec ? of_type(std::false_type{}, std::true_type{}) : of_type(std::false_type{}, std::false_type{});
-    return hipGetLastError() == hipSuccess ? GEMM_RS_OK : GEMM_RS_ERR_HIP;
+    return e == hipSuccess ? GEMM_RS_OK : GEMM_RS_ERR_HIP;
 }
 
 int gemm_q8_query(gemm_q8_plan_t p, gemm_q8_info_t *info) {
