@@ -3,10 +3,14 @@ import numpy as np
 import pytest
 import torch
 
+import oracle as O
 from oracle import ffn as OF
 from tensor_gemm_reduce_lds_amd import ffn as F
+from tensor_gemm_reduce_lds_amd import gemm_rs as G
+from tensor_gemm_reduce_lds_amd import inputs as I
 
-from gpu_util import say
+from gpu_util import (check_tolerance, desc_fields, new_out, oracle_kw, out_to_f64, run_checked, say,
+                      to_device)
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +68,39 @@ def test_int8_norm_writes_no_padding_where_rows_have_no_room():
         torch.cuda.synchronize()
     assert bool((q[5000:] == 77).all())
     assert bool((q[:5000].view(5, 1000).int().abs().amax(1) == 127).all())
+
+
+@pytest.mark.parametrize("M", [800, 8])
+def test_a_ranks_row_chunk_into_the_norm(M):
+    """The rows that the reduce-scatter leaves on each rank go to the norm as
+    the block's output, as they lie in `out`: bounds for the norm's results
+    given these rows (those of its own test), and the rows against the oracle."""
+    W, N = 8, 512
+    w = I.with_shape(I.WORKLOADS["llama70b"], W=W, M=M, N=N, K=256, tile_m=256 if M > 8 else 64, tile_n=256 if M > 8 else 128)
+    x = I.make_inputs(w)
+    out = new_out(w)
+    say("gemm_rs, norm", M)
+    dev = to_device(x, w)
+    with G.Plan(**desc_fields(w)) as plan:
+        run_checked(plan, dev, w, out)
+    check_tolerance(out_to_f64(out, w), O.reference_rows(x["A"], x["B"], x["C"], **oracle_kw(w)), w.dtype)
+    g = torch.Generator().manual_seed(M)
+    rows = M // W
+    stream = torch.randn((M, N), generator=g).bfloat16().cuda()
+    w_post, w_pre = (1 + 0.1 * torch.randn((2, N), generator=g)).cuda()
+    gate = (1 + 0.1 * torch.randn((1, N), generator=g)).cuda()
+    x_out, u = torch.full_like(stream, float("nan")), torch.full_like(stream, float("nan"))
+    y = out.view(torch.bfloat16)
+    s = torch.cuda.current_stream()
+    kw = dict(rows_per_gate=rows, res_scale=0.5)
+    with F.BlockNormPlan(rows, N, **kw) as norm:
+        for r in range(W):
+            c = slice(r * rows, (r + 1) * rows)
+            norm.run(stream[c], y[c], w_post, gate, w_pre, x_out[c], u[c], stream=s)
+        torch.cuda.synchronize()
+    x64 = _f64(stream)
+    want_x, want_u = OF.norm_forward(x64, _f64(y), _f64(w_post), _f64(gate), _f64(w_pre), **dict(kw, rows_per_gate=M))
+    root = np.sqrt((want_x ** 2).mean(1, keepdims=True) + 1e-6)
+    assert (np.abs(_f64(x_out) - want_x) <= 2.0 ** -8 * np.abs(want_x) + FLOAT * (np.abs(x64) + np.abs(want_x))).all()
+    mag = np.abs(want_u) + (np.abs(x64) + np.abs(want_x)) / root * np.abs(_f64(w_pre))
+    assert (np.abs(_f64(u) - want_u) <= 2.0 ** -8 * np.abs(want_u) + FLOAT * mag).all()
