@@ -8,13 +8,12 @@
 #include <atomic>
 #include <type_traits>
 
+#include "ffn_rules.h"
 #include "gemm_rs.h"
 #include "join_slots.h"
 
 namespace gemm_rs {
 namespace ffn {
-
-constexpr int kCus = 256;   // MI355X: 8 XCDs x 32 CUs
 
 // The result of a HIP call.  An error is returned and not left behind as the
 // thread's last one, which a later call, also of another library, would report

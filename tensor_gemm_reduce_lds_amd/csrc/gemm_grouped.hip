@@ -11,7 +11,6 @@
 // have few (8000 rows, 64 experts of 4096 x 1792: 220 us, 4.7 TB/s; 128 rows, 8
 // experts of 4096 x 3584: 44 us, 5.4 TB/s, part of it from the caches; gradients
 // of 44 experts of 4040 x 2048 in 32 bits, 164 rows: 223 us, 6.5 TB/s).
-#include <math.h>
 #include <stdlib.h>
 
 #include "gemm_grouped.h"
@@ -545,98 +544,18 @@ __global__ __launch_bounds__(256) void grouped_join_kernel(GroupedArgs p) {
     }
 }
 
-double ceil_div(double a, double b) { return ceil(a / b); }
-
-// Row tiles of bm rows, as far as the host can tell: every expert with rows
-// has one that is half empty.
-double row_tiles(const GroupedArgs &a, int bm) {
-    const double live = a.E < a.rows ? a.E : a.rows;
-    const double t = (double)a.rows / bm + live / 2;
-    return t > live ? t : live;
-}
-
-// NN and NT: the tile with the least time, which is taken as rounds of 256
-// workgroups (a round costs about as much where it is not full) times the steps
-// of 64 times `step`, plus `fixed` (the first loads, the last stores, waiting
-// for the memory that all of them want at once), in us, but not less than the
-// operands take from memory.  step and fixed are fitted to the times of 170
-// calls of 1..16384 rows, sizes 256..4096, 1..64 experts, where the choice is 1%
-// slower than the best on average.  Large tiles do the most work per byte, small
-// ones fill the CUs; of equals the larger, which reads B less often where an
-// expert has more rows than the mean.  Measured, us for 256 x 256, 128 x 256,
-// 128 x 128 (deep loads, one workgroup per CU / two per CU), 64 x 128, 32 x 64
-// streams (rows : K : N : E): 16384 : 4096 : 3584 : 8 435, 500, 576 / 509, 679,
-// 1420; 8000 : 4096 : 1792 : 64 235, 224, 245 / 237, 266, 463; 10807 : 896 : 1408 :
-// 1 51, 40, 46 / 37, 46, 144; 512 : 4096 : 3584 : 8 75, 69, 50 / 53, 74, 88; 1160 :
-// 1088 : 960 : 6 26, 18, 12 / 13, 10, 18; 128 : 2048 : 1024 : 1 26, 27, 17 / 18, 13,
-// 8.4.
 template <int OP>
 hipError_t launch_rows(GroupedArgs &a, hipStream_t s) {
-    struct Option {
-        int bm, bn;
-        double step, fixed;
-    };
-    const Option options[] = {{256, 256, 1.76, 15.6}, {128, 256, 1.13, 8.0}, {128, 128, 0.71, 1.3},
-                              {64, 128, 0.47, 1.4}, {32, 64, 0.22, 1.4}};
-    const double live = a.E < a.rows ? a.E : a.rows, steps = ceil_div((double)a.K, 64);
-    const double floor_us = 2.0 * (live * a.K * a.N + (double)a.rows * (a.K + a.N)) / 5.0e6;
-    int best = 0;
-    double best_us = 0, best_rounds = 0;
-    for (int i = 0; i < 5; ++i) {
-        const Option &o = options[i];
-        const double rounds = ceil_div(row_tiles(a, o.bm) * ceil_div((double)a.N, o.bn), kCus);
-        double us = rounds * (steps * o.step + o.fixed);
-        if (us < floor_us) us = floor_us;
-        if (i == 0 || us < 0.97 * best_us) {
-            best = i;
-            best_us = us;
-            best_rounds = rounds;
-        }
-    }
-    switch (best) {
-    case 0: return launch_tile<OP, 256, 256, 2, 4, 2, 3>(a, s);
-    case 1: return launch_tile<OP, 128, 256, 2, 4, 3, 3>(a, s);
-    case 2:
-        if (best_rounds > 1) return launch_tile<OP, 128, 128, 2, 2, 2, 3>(a, s);
-        return launch_tile<OP, 128, 128, 2, 4, 4, 4>(a, s);
-    case 3: return launch_tile<OP, 64, 128, 2, 2, 3, 3>(a, s);
+    switch (rows_choice(a.rows, a.K, a.N, a.E)) {
+    case kRows256: return launch_tile<OP, 256, 256, 2, 4, 2, 3>(a, s);
+    case kRows128x256: return launch_tile<OP, 128, 256, 2, 4, 3, 3>(a, s);
+    case kRows128: return launch_tile<OP, 128, 128, 2, 2, 2, 3>(a, s);
+    case kRows128Deep: return launch_tile<OP, 128, 128, 2, 4, 4, 4>(a, s);
+    case kRows64x128: return launch_tile<OP, 64, 128, 2, 2, 3, 3>(a, s);
     default: return launch_stream<OP>(a, s);
     }
 }
 
-// TN: 256 x 256 tiles, which read the rows half as often, or 128 x 128 with two
-// workgroups per CU, so that one stores while the other loads.  With four rounds
-// of large tiles or more these are as fast where the caches hold the rows and
-// faster where they do not, as behind other work (us after a pass over 1 GB, for
-// 256 / 128: 6001 rows, 32 experts of 2048 x 1792 in 32 bits 136 / 165, 8000 rows,
-// 64 experts of 4096 x 1792 in bfloat16 321 / 404); with fewer rounds the small
-// ones lose less in the last (1992 rows, 9 experts of 1920 x 1840 in 32 bits 44 /
-// 40 without that pass), unless groups are long (2048 rows, 8 experts of 4096 x
-// 3584 422 / 565).  With few of the small ones too, `parts` workgroups share a
-// tile's rows and a second kernel adds them, as many as take the least time,
-// from about 0.5 us per step of 64 rows, and for the second kernel 4 us and the
-// parts' traffic (16030 rows, 1296 x 304, 2 experts: 1 part 76 us, 4 38, 8 32; 7984
-// rows, 768 x 512, 8 experts: 1 part 20 us, 2 26).
-struct TnChoice {
-    bool large;
-    int parts;
-};
-TnChoice tn_choice(int64_t rows, int64_t K, int64_t N, int64_t E) {
-    const int64_t large = E * ((K + 255) / 256) * ((N + 255) / 256);
-    const int64_t small = E * ((K + 127) / 128) * ((N + 127) / 128);
-    if (large >= 4 * kCus || (large >= kCus && rows / E >= 448)) return {true, 1};
-    const double steps = (double)(rows / E) / 64, part_us = (double)E * K * N * 8 / 6.0e6;
-    int parts = 1;
-    double best_us = 0.5 * steps;
-    for (int p = 2; p <= 16 && p * small <= 2 * kCus; ++p) {
-        const double us = 0.5 * steps / p + 4 + p * part_us;
-        if (us < best_us) {
-            parts = p;
-            best_us = us;
-        }
-    }
-    return {false, parts};
-}
 // Weight gradients are many times the caches' size, so they are stored past them,
 // and the caches keep the rows (6001 rows, 32 experts of 2048 x 1792 in 32 bits:
 // 111 us, 165 through them; 164 rows, 44 experts of 4040 x 2048: 223, 292).  Such

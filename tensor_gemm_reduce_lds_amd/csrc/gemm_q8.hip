@@ -273,44 +273,21 @@ hipError_t launch_rows(const Q8Args &q, hipStream_t s) {
     return launch_lds<q8_rows_kernel<MB, NB, NW, S>>((q.N + NB * 16 - 1) / (NB * 16), NW * 64, R::LDS_BYTES, s, q);
 }
 
-// Up to 64 rows the product is bound by streaming w: as many workgroups as
-// there are CUs, so 32 channels each where that still makes 256 of them (the
-// rows of a are then read half as often), else 16.  Measured, us for 16 / 32
-// channels: 64 x 8192 x 3584 11.7 / 9.7, 64 x 3584 x 8192 10.5 / 14.1.  From 65
-// rows on the tiles are as fast or faster (128 rows in such streams against
-// 64 x 64 tiles: 128 x 8192 x 3584 14.6 / 11.5, 128 x 3584 x 8192 17.8 / 18.6,
-// 71 x 5241 x 6656 26.4 / 17.6; 64 rows: 64 x 3584 x 8192 10.4 / 18.2).
-template <int MB, int NW1, int S1, int NW2, int S2>
-hipError_t launch_few(const Q8Args &q, hipStream_t s) {
-    if (q.N >= 32 * kCus) return launch_rows<MB, 2, NW2, S2>(q, s);
-    return launch_rows<MB, 1, NW1, S1>(q, s);
-}
-
 hipError_t launch_product(const Q8Args &q, hipStream_t s) {
-    if (q.M <= 16) return launch_few<1, 8, 4, 8, 3>(q, s);
-    if (q.M <= 32) return launch_few<2, 8, 3, 8, 2>(q, s);
-    if (q.M <= 64) return launch_few<4, 8, 2, 4, 3>(q, s);
-    // The tile with the least time, from the rounds of 256 workgroups that it
-    // makes (a round costs about as much where it is not full) and times
-    // measured at K = 3584, in us.  Large tiles read fewer bytes per operation,
-    // small ones fill the CUs when there are few.  One round takes deep loads
-    // and one workgroup per CU, more rounds two or three per CU.  Measured, us
-    // for 256 x 256, 128 x 128 (deep / two per CU), 64 x 128 (deep / three), 64 x
-    // 64: 8192 x 8192 x 3584 236, 354 / 306, 359 / -, 422; 1024 x 3584 x 8192 78,
-    // 39 / 44, 44 / 46, 57; 512 x 3584 x 8192 78, 31 / 38, 27 / 39, 28; 256 x 3584
-    // x 8192 76, 30 / -, 24 / -, 19; 1000 x 4104 x 1792 -, 24 / 21, - / 18, 21.
-    auto rounds = [&](int64_t bm, int64_t bn) {
-        return (double)((((q.M + bm - 1) / bm) * ((q.N + bn - 1) / bn) + kCus - 1) / kCus);
-    };
-    const double r128 = rounds(128, 128), r64w = rounds(64, 128);
-    const double t256 = 59 * rounds(256, 256), t128 = r128 <= 1 ? 18 : 20 * r128;
-    const double t64w = r64w <= 1 ? 13 : 4 + 11 * r64w, t64 = 2 + 8 * rounds(64, 64);
-    if (t256 <= t128 && t256 <= t64w && t256 <= t64) return launch_tile<256, 256, 2, 4, 2, 2>(q, s);
-    if (t128 <= t64w && t128 <= t64)
-        return r128 <= 1 ? launch_tile<128, 128, 2, 4, 4, 4>(q, s) : launch_tile<128, 128, 2, 4, 2, 3>(q, s);
-    if (t64w <= t64)
-        return r64w <= 1 ? launch_tile<64, 128, 2, 2, 3, 3>(q, s) : launch_tile<64, 128, 2, 2, 2, 2>(q, s);
-    return launch_tile<64, 64, 2, 2, 4, 4>(q, s);
+    switch (q8_choice(q.M, q.N)) {
+    case kQ8Rows16: return launch_rows<1, 1, 8, 4>(q, s);
+    case kQ8Rows16Wide: return launch_rows<1, 2, 8, 3>(q, s);
+    case kQ8Rows32: return launch_rows<2, 1, 8, 3>(q, s);
+    case kQ8Rows32Wide: return launch_rows<2, 2, 8, 2>(q, s);
+    case kQ8Rows64: return launch_rows<4, 1, 8, 2>(q, s);
+    case kQ8Rows64Wide: return launch_rows<4, 2, 4, 3>(q, s);
+    case kQ8Tile256: return launch_tile<256, 256, 2, 4, 2, 2>(q, s);
+    case kQ8Tile128: return launch_tile<128, 128, 2, 4, 2, 3>(q, s);
+    case kQ8Tile128Deep: return launch_tile<128, 128, 2, 4, 4, 4>(q, s);
+    case kQ8Tile64x128: return launch_tile<64, 128, 2, 2, 2, 2>(q, s);
+    case kQ8Tile64x128Deep: return launch_tile<64, 128, 2, 2, 3, 3>(q, s);
+    default: return launch_tile<64, 64, 2, 2, 4, 4>(q, s);
+    }
 }
 
 int validate(const gemm_q8_desc_t &d) {
@@ -403,12 +380,13 @@ int gemm_q8_quantize(const void *x, int32_t dtype, int64_t rows, int64_t cols, i
     };
     auto of_type = [&](auto f32, auto wide) {
         constexpr bool F = decltype(f32)::value, W = decltype(wide)::value;
-        // a wave per row where there are many short rows, else a workgroup
-        if (cols <= 2048 && rows >= kCus) go(quantize_kernel<F, W, 32, 64>, 64);
-        else if (cols <= 2048) go(quantize_kernel<F, W, 8, 256>, 256);
-        else if (cols <= 8192) go(quantize_kernel<F, W, 16, 512>, 512);
-        else if (cols <= 16384) go(quantize_kernel<F, W, 16, 1024>, 1024);
-        else go(quantize_kernel<F, W, 0, 256>, 256);
+        switch (quant_choice(rows, cols)) {
+        case kQuantWave: return go(quantize_kernel<F, W, 32, 64>, 64);
+        case kQuant2048: return go(quantize_kernel<F, W, 8, 256>, 256);
+        case kQuant8192: return go(quantize_kernel<F, W, 16, 512>, 512);
+        case kQuant16384: return go(quantize_kernel<F, W, 16, 1024>, 1024);
+        default: return go(quantize_kernel<F, W, 0, 256>, 256);
+        }
     };
     if (dtype == GEMM_RS_F32) vec ? of_type(std::true_type{}, std::true_type{}) : of_type(std::true_type{}, std::false_type{});
     else vec ? of_type(std::false_type{}, std::true_type{}) : of_type(std::false_type{}, std::false_type{});
