@@ -97,9 +97,10 @@ GEMM_RS_API int gemm_grouped_run(gemm_grouped_plan_t plan, const void *A, const 
                                  const void *offsets, void *C, int64_t rows, void *stream);
 
 /*
- * gemm_grouped_status: synchronise `stream`, return the first error that a
- * run recorded (OK, or PROTOCOL for offsets that had to be clipped, with
- * detail {code, expert, offsets[e], offsets[e+1]}), and clear it.  After an
+ * gemm_grouped_status: synchronise `stream`, return the error that a run
+ * recorded since the last call (OK, or PROTOCOL for offsets that had to be
+ * clipped, with detail {code, expert, offsets[e], offsets[e+1]} of one such
+ * expert of the first such run), and clear it.  After an
  * error the outputs of that run are undefined.
  */
 GEMM_RS_API int gemm_grouped_status(gemm_grouped_plan_t plan, void *stream, int32_t *detail4);

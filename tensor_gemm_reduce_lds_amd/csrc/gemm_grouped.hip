@@ -48,8 +48,8 @@ __device__ __forceinline__ void group_rows(const GroupedArgs &p, int e, int32_t 
     *hi = h;
 }
 
-// Run by one wave of a launch: records the first expert whose offsets had to
-// be clipped.
+// Run by one wave of a launch: records an expert whose offsets had to be clipped
+// (of several, whichever lane's exchange comes first), unless one is recorded.
 __device__ __forceinline__ void check_offsets(const GroupedArgs &p) {
     for (int e = threadIdx.x; e < p.E; e += 64) {
         const int32_t a = p.offsets[e], b = p.offsets[e + 1];
