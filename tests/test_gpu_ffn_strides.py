@@ -79,3 +79,24 @@ def test_every_stride_is_its_own(rows, cols, step, types):
         close(got[k], ref, (FLOAT + (rows * EPS24 if sums else FLOAT)) * mag, rel, k)
     a.gaps(dx)
     a.gaps(dy)
+
+
+@pytest.mark.parametrize("post", [0, 1])
+@pytest.mark.parametrize("cols", [5, 513, 1029, 4097, 8191, 16383])
+def test_in_place_on_rows_of_any_length(cols, post):
+    """x' over x where a row's last columns are read together with their
+    neighbours', which another wave may have overwritten by then."""
+    say("norm in place", cols, post)
+    g = torch.Generator().manual_seed(cols)
+    x, y = (torch.randn((70, cols), generator=g).bfloat16().cuda() for _ in range(2))
+    w = (1 + 0.1 * torch.randn((2, cols), generator=g)).cuda()
+    s = torch.cuda.current_stream()
+    with F.BlockNormPlan(70, cols, post=post) as plan:
+        outs = []
+        for to in (torch.empty_like(x), x.clone()):
+            src = x if not outs else to
+            u = torch.empty_like(x)
+            plan.run(src, y, w[0] if post else None, None, w[1], to, u, stream=s)
+            outs.append((to, u))
+        torch.cuda.synchronize()
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
