@@ -67,7 +67,8 @@ extern "C" {
  *   pad            must be 0
  * Any size, stride and element-aligned address is accepted; rows whose
  * lengths, strides and addresses are all multiples of 8 elements (16 bytes)
- * are faster (8192 rows of 8192 columns forward 100 us, of 8191 120).
+ * are faster (8192 rows of 8192 columns forward 98 us, of 8191 116; backward 168
+ * and 214).
  */
 typedef struct block_norm_desc {
     int64_t rows, cols;

@@ -51,9 +51,11 @@ extern "C" {
  *               after the one before.
  *   pad         must be 0
  * Any sizes and element-aligned addresses are accepted.  Sizes, strides and
- * addresses that are all multiples of 8 elements (16 bytes) take the kernels
- * with direct loads to shared memory, others a kernel that takes about twice as
- * long (8000 rows, 64 experts of 4095 x 1791: 500 us, of 4096 x 1792: 220).
+ * addresses that are all multiples of 8 elements (16 bytes; ldc of floats of 4)
+ * take the kernels with direct loads to shared memory, others, also where C
+ * alone is not aligned, a kernel that takes 2 to 3.5 times as long (even groups,
+ * 8000 rows, 64 experts of 4095 x 1791: 450 us, of 4096 x 1792: 190; 16384 rows, 8
+ * experts of 4095 x 3583: 1.4 ms, of 4096 x 3584: 0.4).
  */
 typedef struct gemm_grouped_desc {
     int64_t M, N, K;

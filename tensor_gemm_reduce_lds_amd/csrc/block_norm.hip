@@ -4,8 +4,9 @@
 // at a time, the whole row in registers: one read of x and y, one write of x'
 // and u.  Two joins over the workgroup (the mean square of y, then of x', which
 // needs the first), a third for the largest |u| when u is quantised.
-// 8000 x 8192, f32 stream: 148 us, 5.3 TB/s (a large copy on the same card runs
-// at 4.95 TB/s).
+// 8000 x 8192, f32 stream: 147 us, 5.4 TB/s; 8192 x 8192 bf16: 98 us, 5.5 TB/s (on
+// the same card a copy runs at 4.9 TB/s, two reads and a write at 5.9, writes
+// alone at 6.9).
 //
 // Backward: a workgroup walks a run of consecutive rows (loading one row while
 // it works on the one before, where that helps) and keeps the sums for dw_post,
@@ -13,8 +14,12 @@
 // of x' and y and the product a.x' together, then b.y).  The partial sums go to
 // the workspace once per workgroup and a second kernel adds them in a fixed
 // order (6 to 7 us).
-// 8192 x 8192 bf16: 165 us, 4.9 TB/s; 1000 x 4096, f32 stream: 23 us (few rows
-// per workgroup, and the partial sums are a third of the traffic).
+// 8192 x 8192 bf16: 168 us with the joining kernel, 4.8 TB/s; 1000 x 4096, f32
+// stream: 25 us (few rows per workgroup, and the partial sums are a third of the
+// traffic).
+//
+// Times in this file are of whole calls in a stream, several sets of inputs in
+// turn that together exceed the caches, unless they say otherwise.
 #include <math.h>
 #include <stdlib.h>
 
@@ -206,7 +211,7 @@ struct Own<EPT, THREADS, true> {
     __device__ __forceinline__ void set(int i, float x) { at[i / 4 * THREADS][i % 4] = x; }
 };
 // Rows of more than 8192 columns keep w_pre and the sums for dw_post in LDS
-// (8192 x 16384 bf16: 1449 us with all in registers and spills, 390).
+// (8192 x 16384 bf16: 429 us, with all in registers and spills 1224).
 template <int EPT, int THREADS>
 constexpr bool kOwnInLds = EPT * THREADS > 8192;
 
@@ -476,11 +481,13 @@ hipError_t launch_forward(const NormArgs &a, bool sf, bool yf, bool quant, int64
 
 template <bool WIDE, int EPT, int THREADS>
 hipError_t launch_backward(const NormArgs &a, bool sf, bool yf, int64_t grid, hipStream_t s) {
-    // The next row is loaded ahead where its rows are aligned and registers are
-    // left for it (8192 x 8192 bf16: 122 us, 137 without; 4096 columns 67, 87).
-    // Unaligned rows need more registers as it is: float streams lose what bf16
-    // gains (4096 x 8191 in float 118 us, 137 with the next row ahead; 8192 x
-    // 8191 in bf16 199, 176).
+    // The next row is loaded ahead where rows are aligned and registers are left
+    // for it (8192 rows in bf16, ahead / not: 8192 columns 168 / 173 us, 4096
+    // columns 88 / 108, 2048 columns 51 / 49).  Unaligned rows need more registers
+    // as it is, which a workgroup's only row pays for and many rows would gain by
+    // (kernels in a graph, 8 x 8191 in float 11.8 / 10.8, 255 x 8191 25.3 / 24.4;
+    // 1500 x 8191 61.8 / 65.5; calls, 8192 x 8191 in bf16 187 / 214, 4095 columns
+    // 108 / 130).
     constexpr bool AHEAD = WIDE && !kOwnInLds<EPT, THREADS>;
     constexpr int lds = 2 * Own<EPT, THREADS, kOwnInLds<EPT, THREADS>>::BYTES;
     if (sf && yf) return launch_lds<norm_backward_kernel<WIDE, EPT, THREADS, true, true, AHEAD>>(grid, THREADS, lds, s, a);
@@ -495,9 +502,12 @@ struct Shape {
     static constexpr int EPT = EPT_, THREADS = THREADS_;
 };
 
-// Calls f with the kernel shape of a row length.  Up to 8192 columns: few rows
-// take 1024 threads (the latency of one row), many take 512, which leaves each
-// CU rows to overlap (8192 x 8192 bf16: 115 / 102 us).
+// Calls f with the kernel shape of a row length.  Up to 8192 columns: many rows
+// take 512 threads, which leaves each CU rows to overlap (bf16, 512 / 1024
+// threads: 8192 x 8192 98 / 100 us, 8192 x 8191 116 / 143, 300 x 8191 in a graph
+// 8.6 / 10.5); up to one row per CU take 1024, whose shorter chain per thread
+// serves rows that are not aligned (in a graph, 64 x 8191 5.6 / 5.3, 64 x 8192
+// 4.1 / 4.3).
 template <class F>
 void forward_shape(int64_t rows, int64_t cols, F f) {
     if (cols <= 512) f(Shape<8, 64>{});

@@ -42,6 +42,8 @@ inline Q8Choice q8_choice(int64_t M, int64_t N) {
     // 64: 8192 x 8192 x 3584 236, 354 / 306, 359 / -, 422; 1024 x 3584 x 8192 78,
     // 39 / 44, 44 / 46, 57; 512 x 3584 x 8192 78, 31 / 38, 27 / 39, 28; 256 x 3584
     // x 8192 76, 30 / -, 24 / -, 19; 1000 x 4104 x 1792 -, 24 / 21, - / 18, 21.
+    // (K does not enter: a tile's fixed part, its first loads and last stores,
+    // weighs more in a short contraction than these times have it.)
     auto rounds = [&](int64_t bm, int64_t bn) {
         return (double)((((M + bm - 1) / bm) * ((N + bn - 1) / bn) + kCus - 1) / kCus);
     };
@@ -67,22 +69,26 @@ inline QuantChoice quant_choice(int64_t rows, int64_t cols) {
 // ---- products grouped by expert, NN and NT ------------------------------------
 enum RowsChoice { kRows256, kRows128x256, kRows128, kRows128Deep, kRows64x128, kRowsStream, kRowsChoices };
 
-// The tile with the least time, which is taken as rounds of 256 workgroups (a
-// round costs about as much where it is not full) times the steps of 64 times
-// `step`, plus `fixed` (the first loads, the last stores, waiting for the memory
-// that all of them want at once), in us, but not less than the operands take from
-// memory.  Row tiles are counted as far as the host can tell: every expert with
-// rows has one that is half empty.  step and fixed are fitted to the times of 170
-// calls of 1..16384 rows, sizes 256..4096, 1..64 experts, where the choice is 1%
-// slower than the best on average.  Large tiles do the most work per byte, small
-// ones fill the CUs; of equals the larger, which reads B less often where an
-// expert has more rows than the mean.  Measured, us for 256 x 256, 128 x 256,
-// 128 x 128 (deep loads, one workgroup per CU / two per CU), 64 x 128, 32 x 64
-// streams (rows : K : N : E): 16384 : 4096 : 3584 : 8 435, 500, 576 / 509, 679,
-// 1420; 8000 : 4096 : 1792 : 64 235, 224, 245 / 237, 266, 463; 10807 : 896 : 1408 :
-// 1 51, 40, 46 / 37, 46, 144; 512 : 4096 : 3584 : 8 75, 69, 50 / 53, 74, 88; 1160 :
-// 1088 : 960 : 6 26, 18, 12 / 13, 10, 18; 128 : 2048 : 1024 : 1 26, 27, 17 / 18, 13,
-// 8.4.
+// The tile with the least time, which is taken as rounds of 256 workgroups (a round
+// costs about as much where it is not full) times the steps of 64 times `step`,
+// plus `fixed` (the first loads, the last stores, waiting for the memory that all
+// of them want at once), in us, but not less than the operands take at 5 TB/s, a
+// copy's rate.  Row tiles are counted as far as the host can tell: every expert
+// with rows has one that is half empty; what other splits cost over even ones
+// (16384 rows, 8 experts of 4096 x 3584, one with half of the rows 416 us, with all
+// 391, even 406; 8000 rows, 64 experts of 4096 x 1792, one with half 220, 8 with
+// three quarters 232, even 188) is their row tiles.  step and fixed are fitted to
+// the times of 170 calls of 1..16384 rows, sizes 256..4096, 1..64 experts, where
+// the choice is 1% slower than the best on average.  These and the following are
+// times of calls repeated on the same operands, part of which the caches hold.
+// Large tiles do the most work per byte, small ones fill the CUs; of equals the
+// larger, which reads B less often where an expert has more rows than the mean.
+// Measured, us for 256 x 256, 128 x 256, 128 x 128 (deep loads, one workgroup per
+// CU / two per CU), 64 x 128, 32 x 64 streams (rows : K : N : E): 16384 : 4096 :
+// 3584 : 8 435, 500, 576 / 509, 679, 1420; 8000 : 4096 : 1792 : 64 235, 224, 245 /
+// 237, 266, 463; 10807 : 896 : 1408 : 1 51, 40, 46 / 37, 46, 144; 512 : 4096 : 3584
+// : 8 75, 69, 50 / 53, 74, 88; 1160 : 1088 : 960 : 6 26, 18, 12 / 13, 10, 18; 128 :
+// 2048 : 1024 : 1 26, 27, 17 / 18, 13, 8.4.
 inline RowsChoice rows_choice(int64_t rows, int64_t K, int64_t N, int64_t E) {
     struct Option {
         int bm, bn;
@@ -118,18 +124,22 @@ inline RowsChoice rows_choice(int64_t rows, int64_t K, int64_t N, int64_t E) {
 
 // ---- products grouped by expert, TN -------------------------------------------
 // 256 x 256 tiles, which read the rows half as often, or 128 x 128 with two
-// workgroups per CU, so that one stores while the other loads.  With four rounds
-// of large tiles or more these are as fast where the caches hold the rows and
-// faster where they do not, as behind other work (us after a pass over 1 GB, for
-// 256 / 128: 6001 rows, 32 experts of 2048 x 1792 in 32 bits 136 / 165, 8000 rows,
-// 64 experts of 4096 x 1792 in bfloat16 321 / 404); with fewer rounds the small
-// ones lose less in the last (1992 rows, 9 experts of 1920 x 1840 in 32 bits 44 /
-// 40 without that pass), unless groups are long (2048 rows, 8 experts of 4096 x
-// 3584 422 / 565).  With few of the small ones too, `parts` workgroups share a
-// tile's rows and a second kernel adds them, as many as take the least time,
-// from about 0.5 us per step of 64 rows, and for the second kernel 4 us and the
-// parts' traffic (16030 rows, 1296 x 304, 2 experts: 1 part 76 us, 4 38, 8 32; 7984
-// rows, 768 x 512, 8 experts: 1 part 20 us, 2 26).
+// workgroups per CU, so that one stores while the other loads.  With four rounds of
+// large tiles or more these are as fast where the caches hold the rows and faster
+// where they do not, as behind other work (us after a pass over 1 GB, for 256 /
+// 128: 6001 rows, 32 experts of 2048 x 1792 in 32 bits 136 / 165, 8000 rows, 64
+// experts of 4096 x 1792 in bfloat16 321 / 404, 16384 rows, 8 experts of 4096 x
+// 3584 427 / 570).  With one to four rounds they mostly are where groups are long,
+// as the last round counts less (the same in bfloat16, 8 experts of 2048 x 2048, 512
+// tiles: 448 rows each 45 / 58, 1024 77 / 99; of 1536 x 1536, 288 tiles: 448 rows
+// 40 / 39, 1024 70 / 65, 4096 222 / 213, but repeated on the same rows 168 / 196);
+// with shorter groups it depends (221 rows each, 9 experts of 1920 x 1840: 48 / 44,
+// repeated 35 / 31; 256 rows each, 8 experts of 2048 x 2048: 36 / 47, repeated 28 /
+// 31).  With few of the small ones too, `parts` workgroups share a tile's rows and
+// a second kernel adds them, as many as take the least time, from about 0.5 us per
+// step of 64 rows, and for the second kernel 4 us and the parts' traffic (16030
+// rows, 1296 x 304, 2 experts: 1 part 76 us, 4 38, 8 32; 7984 rows, 768 x 512, 8
+// experts: 1 part 20 us, 2 26).
 struct TnChoice {
     bool large;
     int parts;

@@ -8,9 +8,10 @@
 // Bound by the matrix pipe at the board's power limit where experts have many
 // rows (16384 rows, 8 experts of 4096 x 3584: product 437 us, 1100 TFLOP/s,
 // gradients 466 and 420 us), by reading B or writing weight gradients where they
-// have few (8000 rows, 64 experts of 4096 x 1792: 220 us, 4.7 TB/s; 128 rows, 8
-// experts of 4096 x 3584: 44 us, 5.4 TB/s, part of it from the caches; gradients
-// of 44 experts of 4040 x 2048 in 32 bits, 164 rows: 223 us, 6.5 TB/s).
+// have few (8000 rows in uneven groups, 64 experts of 4096 x 1792, inputs in turn:
+// 218 us, 4.7 TB/s; 128 rows, 8 experts of 4096 x 3584: 44 us, 5.4 TB/s, part of it
+// from the caches; gradients of 44 experts of 4040 x 2048 in 32 bits, 164 rows: 223
+// us, 6.5 TB/s).
 #include <stdlib.h>
 
 #include "gemm_grouped.h"
@@ -198,9 +199,11 @@ __device__ __forceinline__ i32x4_t fragment(lds_t *tile, int m, int ks) {
 // outputs per workgroup, 32 x 32 per wave, 64 of the contraction at a time,
 // loaded through registers (16 bytes at any element address, zeros outside the
 // operand) two steps ahead, and written to the other of two LDS buffers one step
-// ahead.  8000 rows, 64 experts of 4095 x 1791: product and gradient of x 500 us,
-// 235 TFLOP/s; loads of single elements took 2350.  Bound by the latency of a
-// step, as a tile of this size has few loads to run ahead.
+// ahead.  Even groups, repeated calls: 8000 rows, 64 experts of 4095 x 1791: product
+// and gradient of x 450 us, 260 TFLOP/s (loads of single elements took 2350), of
+// 4096 x 1792 in the tiles below 190 and 200; 16384 rows, 8 experts of 4095 x 3583 1.4 ms, 340 TFLOP/s, of
+// 4096 x 3584 0.4.  Bound by the latency of a step, as a tile of this size has few
+// loads to run ahead.
 template <int OP>
 __global__ __launch_bounds__(256) void grouped_narrow_kernel(GroupedArgs p) {
     constexpr bool A_COL = OP == GEMM_GROUPED_TN, B_COL = OP != GEMM_GROUPED_NT;
@@ -557,13 +560,16 @@ hipError_t launch_rows(GroupedArgs &a, hipStream_t s) {
 }
 
 // Weight gradients are many times the caches' size, so they are stored past them,
-// and the caches keep the rows (6001 rows, 32 experts of 2048 x 1792 in 32 bits:
+// and the caches keep the rows (repeated calls: 6001 rows, 32 experts of 2048 x 1792 in 32 bits:
 // 111 us, 165 through them; 164 rows, 44 experts of 4040 x 2048: 223, 292).  Such
 // stores have to cover whole lines (in runs of half a line: 589).  Rows that do
 // not begin on a line break that at each tile's edge, which in 32 bits costs more
 // than few rows per expert gain (20 experts of 1280 x 3576, 32 rows each 115 / 79,
 // 64 rows 114 / 102, 128 rows 112 / 132; in bfloat16 56 / 50, 60 / 58, 74 / 70,
-// but 34 experts of 3648 x 2248, 84 rows each 175 / 234).
+// but 34 experts of 3648 x 2248, 84 rows each 175 / 234).  Adding to C reads it in
+// the epilogue: after a pass over 1 GB, 6001 rows, 32 experts of 2048 x 1792 in
+// bfloat16 93 us, added to 192, in 32 bits 131 and 297; 16384 rows, 8 experts of 4096
+// x 3584 429 and 507, 458 and 600.
 bool stream_stores(const GroupedArgs &a) {
     return !a.out_f32 || (a.ldc % 32 == 0 && aligned(a.C, 128)) || a.rows / a.E >= 96;
 }
