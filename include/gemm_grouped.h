@@ -76,8 +76,8 @@ typedef struct gemm_grouped_info {
  * gemm_grouped_plan: validate and allocate.  Returns OK, INVALID_ARG (NULL
  * pointers, M, N, K or E < 1, unknown op or type, accumulate other than 0/1
  * or without TN, strides below the row length, pad), UNSUPPORTED (E above
- * 1024, M, N or K of 2^31 or more, strides of 2^23 or more, a grid over
- * 2^31-1) or HIP.  Rejected before any HIP call.
+ * 1024, M above 2^31-1025, N, K or strides of 2^23 or more, a grid over 2^31-1)
+ * or HIP.  Rejected before any HIP call.
  */
 GEMM_RS_API int gemm_grouped_plan(const gemm_grouped_desc_t *desc, gemm_grouped_plan_t *out);
 

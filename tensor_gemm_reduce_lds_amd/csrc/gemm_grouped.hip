@@ -23,6 +23,9 @@ namespace {
 
 constexpr int64_t kMaxStride = int64_t(1) << 23;
 constexpr int kMaxE = 1024;
+// most rows: the last step of 64 that is begun (some are loaded ahead) ends
+// within 32 bits
+constexpr int64_t kMaxRows = INT32_MAX - 1024;
 
 struct GroupedArgs {
     int64_t rows, N, K, lda, ldb, ldc;
@@ -613,7 +616,7 @@ int validate(const gemm_grouped_desc_t &d) {
     if (d.lda < 0 || d.ldb < 0 || d.ldc < 0 || (d.lda && d.lda < d.K) || (d.ldb && d.ldb < bcols) ||
         (d.ldc && d.ldc < d.N))
         return GEMM_RS_ERR_INVALID_ARG;
-    if (d.E > kMaxE || d.M > INT32_MAX || d.N > INT32_MAX || d.K > INT32_MAX)
+    if (d.E > kMaxE || d.M > kMaxRows || d.N > INT32_MAX || d.K > INT32_MAX)
         return GEMM_RS_ERR_UNSUPPORTED;
     if (d.lda >= kMaxStride || d.ldb >= kMaxStride || d.ldc >= kMaxStride || d.K >= kMaxStride ||
         d.N >= kMaxStride)

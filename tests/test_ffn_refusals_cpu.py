@@ -50,3 +50,14 @@ def test_offsets_of_another_layout_are_refused(kw, ok):
     assert len(calls) == int(ok)
     plan.run(None, None, 4096, None)
     assert len(calls) == 1 + int(ok)
+
+
+def test_rows_whose_last_steps_pass_32_bits_are_unsupported():
+    """Steps of 64 rows are counted in 32 bits, a few past the last one: with 2^31
+    - 1 rows of one expert the end of the last step would be negative."""
+    for m, want in ((2 ** 31 - 1, G.ERR_UNSUPPORTED), (2 ** 31 - 1024, G.ERR_UNSUPPORTED)):
+        with pytest.raises(G.GemmRsError) as e:
+            F.GroupedPlan(m, 8, 8, 1, F.GROUPED_TN)
+        assert e.value.code == want
+    most = 2 ** 31 - 1025
+    assert (-(-most // 64) + 4) * 64 < 2 ** 31
