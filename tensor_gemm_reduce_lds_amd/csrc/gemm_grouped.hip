@@ -535,6 +535,11 @@ __global__ __launch_bounds__(256) void grouped_join_kernel(GroupedArgs p) {
     const int64_t runs = p.N / 8, all = (int64_t)p.E * p.K * runs;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < all; i += (int64_t)gridDim.x * 256) {
         const int64_t row = i / runs, n = i % runs * 8;
+        if (p.accumulate) {          // nothing is added for an expert without rows, not even to -0
+            int32_t lo, hi;
+            group_rows(p, (int)(row / p.K), &lo, &hi);
+            if (hi == lo) continue;
+        }
         float x[8] = {};
 #pragma unroll 4
         for (int s = 0; s < p.parts; ++s) {
