@@ -250,7 +250,7 @@ class GroupedPlan(_Plan):
 
     def run(self, A, B, offsets, C, rows=None, stream=None):
         """offsets: an int32 tensor of E + 1 on the GPU, or an address."""
-        if offsets is not None and offsets.__class__ is not int:
+        if hasattr(offsets, "element_size"):        # (neither an address nor a bare data_ptr())
             _check_offsets(offsets, self._offsets)
         rc = self._run(self.handle, *_addresses(A, B, offsets, C),
                        self._rows if rows is None else rows, _stream_handle(stream))

@@ -52,6 +52,18 @@ def test_offsets_of_another_layout_are_refused(kw, ok):
     assert len(calls) == 1 + int(ok)
 
 
+def test_offsets_may_be_anything_that_has_an_address():
+    class Address:
+        def data_ptr(self):
+            return 4096
+
+    plan, calls = object.__new__(F.GroupedPlan), []
+    plan.handle, plan._rows, plan._offsets = None, 8, 4
+    plan._run = lambda *a: calls.append(a) or G.OK
+    plan.run(None, None, Address(), None)
+    assert calls[0][3] == 4096
+
+
 def test_rows_whose_last_steps_pass_32_bits_are_unsupported():
     """Steps of 64 rows are counted in 32 bits, a few past the last one: with 2^31
     - 1 rows of one expert the end of the last step would be negative."""
