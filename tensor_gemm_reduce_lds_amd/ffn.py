@@ -6,7 +6,9 @@ product with bias, activation and residual (include/gemm_epi.h).
 
 Argument marshalling only, as in ``gemm_rs``: tensors go in as device
 pointers, the stream as its ``hipStream_t`` handle, and a non-OK status
-raises ``GemmRsError`` from the owning wrappers.
+raises ``GemmRsError`` from the owning wrappers.  The plans of the dense
+products, whose arrays have types and strides of their own, refuse tensors
+that do not hold what the plan takes them for; addresses are taken as they are.
 """
 from __future__ import annotations
 
@@ -176,6 +178,25 @@ def _check_offsets(t, n):
         raise GemmRsError(ERR_INVALID_ARG, "gemm_grouped_run: offsets are not %d contiguous int32 on the GPU" % n)
 
 
+def _holds(t, rows, cols, ld):
+    """Whether a tensor's elements lie as `rows` rows of `cols`, ld elements apart."""
+    shape, stride = t.shape, t.stride()
+    if not shape:
+        return rows * cols <= 1
+    if len(shape) == 2 and stride == (ld, 1) and shape[0] >= rows and shape[1] >= cols:
+        return True
+    if shape[-1] > 1 and stride[-1] != 1:
+        return False
+    have = 1                        # rows of the tensor, equally far apart
+    for i in range(len(shape) - 2, -1, -1):
+        if shape[i] > 1 and stride[i] != ld * have:
+            return False
+        have *= shape[i]
+    if have >= rows and shape[-1] >= cols:
+        return True
+    return t.is_contiguous() and t.numel() >= (rows - 1) * ld + cols       # (an array without a shape of its own)
+
+
 class _Plan:
     """Owns one plan handle of the family `_name`."""
 
@@ -301,7 +322,51 @@ class GroupedPlan(_Plan):
         return rc, list(detail)
 
 
-class GatedPlan(_Plan):
+class _DensePlan(_Plan):
+    """A plan that knows its arrays: their types, rows (None: a call's), columns and strides."""
+
+    def __init__(self, desc):
+        super().__init__(desc)
+        self._rows = desc.M
+        self._w = (desc.K, desc.N) if desc.layout == WEIGHTS_KN else (desc.N, desc.K)
+        self._tensor, self._types, self._device = (), {}, 0
+        try:
+            import torch
+        except ImportError:            # (then arrays are addresses)
+            return
+        self._tensor = torch.Tensor
+        self._types = {BF16: (torch.bfloat16, torch.int16, torch.uint16), F32: (torch.float32,)}      # (bfloat16 may come as its bits)
+        if torch.cuda.is_available():
+            self._device = torch.cuda.current_device()
+
+    def _array(self, name, dtype, rows, cols, ld):
+        types = self._types.get(dtype, (None,))
+        # (with the shape that most calls bring, where tight rows are the plan's)
+        return types[0], (self._rows if rows is None else rows, cols) if ld in (0, cols) else None, (name, types, rows, cols, ld or cols)
+
+    def _arrays(self, where, arrays, tensors, rows):
+        """Device addresses of tensors, as `_addresses`.  The kernels know an array by
+        its address alone: one of another type, length or stride, of the host's or of
+        another device would be read and written past its end, so it is refused.
+        It costs 0.3 us an array on the host: one row of 256 x 256, four arrays, takes
+        5.0 us a call instead of 3.7; one of 3584 x 8192 takes the GPU's 10.3 either way."""
+        T, device = self._tensor, self._device
+        return [t if t is None or t.__class__ is int else
+                t.data_ptr() if isinstance(t, T) and t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous() else
+                self._address(where, array, t, rows) for t, (dtype, shape, array) in zip(tensors, arrays)]
+
+    def _address(self, where, array, t, rows):
+        name, types, n, cols, ld = array
+        if isinstance(t, self._tensor):            # (else anything that has an address)
+            if n is None:
+                n = rows
+            if t.dtype not in types or t.get_device() != self._device or not (n <= 0 or _holds(t, n, cols, ld)):
+                raise GemmRsError(ERR_INVALID_ARG, "%s: %s (%s, shape %s, stride %s, %s) is not %d x %d of %s, rows %d apart, on GPU %d" % (
+                    where, name, t.dtype, tuple(t.shape), t.stride(), t.device, n, cols, types[0], ld, self._device))
+        return t.data_ptr()
+
+
+class GatedPlan(_DensePlan):
     """Gated projections, h = act(x w_gate + b_gate) * (x w_up + b_up), and their backward pass."""
 
     _name, _info_t = "gemm_gated", gemm_gated_info_t
@@ -311,23 +376,31 @@ class GatedPlan(_Plan):
         super().__init__(gemm_gated_desc_t(M=M, N=N, K=K, layout=layout, act=act, has_bias=has_bias,
                                            bias_dtype=bias_dtype, backward=backward, dw_dtype=dw_dtype,
                                            accumulate=accumulate, z_dtype=z_dtype, **strides))
-        self._rows = M
+        d, a = self.desc, self._array
+        x, w = a("x", BF16, None, K, d.ldx), [a("w_" + k, BF16, *self._w, d.ldw) for k in ("gate", "up")]
+        z = [a("z_" + k, z_dtype, None, N, d.ldz) for k in ("gate", "up")]
+        self._forward = [x, *w, *(a("b_" + k, bias_dtype, 1, N, 0) for k in ("gate", "up")), a("h", BF16, None, N, d.ldh), *z]
+        self._backward = [a("dh", BF16, None, N, d.lddh), x, *w, *z, *(a("dz_" + k, BF16, None, N, d.lddz) for k in ("gate", "up")),
+                          a("dx", BF16, None, K, d.lddx), *(a("dw_" + k, dw_dtype, *self._w, d.lddw) for k in ("gate", "up")),
+                          *(a("db_" + k, F32, 1, N, 0) for k in ("gate", "up"))]
 
     def run(self, x, w_gate, w_up, b_gate, b_up, h, z_gate=None, z_up=None, rows=None, stream=None):
-        rc = self._run(self.handle, *_addresses(x, w_gate, w_up, b_gate, b_up, h, z_gate, z_up),
-                       self._rows if rows is None else rows, _stream_handle(stream))
+        rows = self._rows if rows is None else rows
+        rc = self._run(self.handle, *self._arrays("gemm_gated_run", self._forward, (x, w_gate, w_up, b_gate, b_up, h, z_gate, z_up), rows),
+                       rows, _stream_handle(stream))
         if rc != OK:
             raise GemmRsError(rc, "gemm_gated_run")
 
     def backward(self, dh, x, w_gate, w_up, z_gate, z_up, dz_gate, dz_up, dx, dw_gate=None, dw_up=None,
                  db_gate=None, db_up=None, rows=None, stream=None):
+        rows = self._rows if rows is None else rows
         _check(self._lib.gemm_gated_backward(
-            self.handle, *_addresses(dh, x, w_gate, w_up, z_gate, z_up, dz_gate, dz_up, dx, dw_gate, dw_up,
-                                     db_gate, db_up),
-            self._rows if rows is None else rows, _stream_handle(stream)), "gemm_gated_backward")
+            self.handle, *self._arrays("gemm_gated_backward", self._backward,
+                                       (dh, x, w_gate, w_up, z_gate, z_up, dz_gate, dz_up, dx, dw_gate, dw_up, db_gate, db_up), rows),
+            rows, _stream_handle(stream)), "gemm_gated_backward")
 
 
-class EpiPlan(_Plan):
+class EpiPlan(_DensePlan):
     """Product with bias, activation and residual, y = act(x w + bias) + r, and its backward pass."""
 
     _name, _info_t = "gemm_epi", gemm_epi_info_t
@@ -338,15 +411,20 @@ class EpiPlan(_Plan):
                                          has_bias=has_bias, bias_dtype=bias_dtype, has_residual=has_residual,
                                          backward=backward, dw_dtype=dw_dtype, accumulate=accumulate,
                                          z_dtype=z_dtype, **strides))
-        self._rows = M
+        d, a = self.desc, self._array
+        x, w, z = a("x", BF16, None, K, d.ldx), a("w", BF16, *self._w, d.ldw), a("z", z_dtype, None, N, d.ldz)
+        self._forward = [x, w, a("bias", bias_dtype, 1, N, 0), a("r", out_dtype, None, N, d.ldr), a("y", out_dtype, None, N, d.ldy), z]
+        self._backward = [a("dy", out_dtype, None, N, d.lddy), x, w, z, a("dz", BF16, None, N, d.lddz), a("dx", BF16, None, K, d.lddx),
+                          a("dw", dw_dtype, *self._w, d.lddw), a("dbias", F32, 1, N, 0)]
 
     def run(self, x, w, bias, r, y, z=None, rows=None, stream=None):
-        rc = self._run(self.handle, *_addresses(x, w, bias, r, y, z),
-                       self._rows if rows is None else rows, _stream_handle(stream))
+        rows = self._rows if rows is None else rows
+        rc = self._run(self.handle, *self._arrays("gemm_epi_run", self._forward, (x, w, bias, r, y, z), rows), rows, _stream_handle(stream))
         if rc != OK:
             raise GemmRsError(rc, "gemm_epi_run")
 
     def backward(self, dy, x, w, z, dz, dx, dw=None, dbias=None, rows=None, stream=None):
+        rows = self._rows if rows is None else rows
         _check(self._lib.gemm_epi_backward(
-            self.handle, *_addresses(dy, x, w, z, dz, dx, dw, dbias),
-            self._rows if rows is None else rows, _stream_handle(stream)), "gemm_epi_backward")
+            self.handle, *self._arrays("gemm_epi_backward", self._backward, (dy, x, w, z, dz, dx, dw, dbias), rows),
+            rows, _stream_handle(stream)), "gemm_epi_backward")
