@@ -25,7 +25,9 @@
  *
  * Activations: GEMM_ACT_NONE (act(z) = z), GEMM_ACT_RELU (its derivative at 0 is
  * 0), GEMM_ACT_GELU (z * Phi(z)), GEMM_ACT_GELU_TANH (its form with tanh) and
- * GEMM_ACT_SILU (z / (1 + exp(-z))), within 1e-5 of their value in floats.
+ * GEMM_ACT_SILU (z / (1 + exp(-z))), in floats within 1e-5 of their value, or 1e-17
+ * where that is more (far out on the negative side), and their derivatives within
+ * 1e-5.
  *
  * Status codes and gemm_rs_strerror are those of gemm_rs.h.  All functions
  * are plain C, never throw, abort or print.
