@@ -108,29 +108,33 @@ __global__ __launch_bounds__(1024) void bias_join_kernel(ActGradArgs p) {
     db[col] = p.add ? db[col] + t : t;
 }
 
-// A wave per row, 16 bytes per lane at any element address.
+// A wave per row, 16 bytes per lane at any element address; every 4 * kCopyGroups-th
+// row where there are more.
+constexpr int64_t kCopyGroups = 1 << 22;
 __global__ __launch_bounds__(256) void padded_copy_kernel(PadArgs p) {
     constexpr int U = 4;                // loads ahead
     const int lane = threadIdx.x & 63;
-    int64_t row = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    int which = 0;
-    while (which < p.count && row >= p.m[which].rows) row -= p.m[which++].rows;
-    if (which == p.count) return;
-    const auto &m = p.m[which];
-    const uint16_t *const from = m.from + row * m.ld;
-    uint16_t *const to = m.to + row * m.to_ld;
-    const uint32_t cols = (uint32_t)m.cols, all = (uint32_t)m.to_ld;
-    for (uint32_t c0 = lane * 8; c0 < all; c0 += U * 512) {
-        Raw<false> r[U];
+    for (int64_t at = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);; at += 4 * kCopyGroups) {
+        int64_t row = at;
+        int which = 0;
+        while (which < p.count && row >= p.m[which].rows) row -= p.m[which++].rows;
+        if (which == p.count) return;
+        const auto &m = p.m[which];
+        const uint16_t *const from = m.from + row * m.ld;
+        uint16_t *const to = m.to + row * m.to_ld;
+        const uint32_t cols = (uint32_t)m.cols, all = (uint32_t)m.to_ld;
+        for (uint32_t c0 = lane * 8; c0 < all; c0 += U * 512) {
+            Raw<false> r[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (c0 + u * 512 < all) fetch8<false, false>(r[u], from, c0 + u * 512, cols);
+            for (int u = 0; u < U; ++u)
+                if (c0 + u * 512 < all) fetch8<false, false>(r[u], from, c0 + u * 512, cols);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t c = c0 + u * 512;
-            if (c >= all) break;
-            settle8<false, false>(r[u], c, cols);
-            *(u32x4_t *)(to + c) = r[u].a;
+            for (int u = 0; u < U; ++u) {
+                const uint32_t c = c0 + u * 512;
+                if (c >= all) break;
+                settle8<false, false>(r[u], c, cols);
+                *(u32x4_t *)(to + c) = r[u].a;
+            }
         }
     }
 }
@@ -175,7 +179,8 @@ hipError_t launch_activation_gradient(ActGradArgs &a, int64_t room, hipStream_t 
 hipError_t launch_padded_copies(const PadArgs &a, hipStream_t s) {
     int64_t rows = 0;
     for (int i = 0; i < a.count; ++i) rows += a.m[i].rows;
-    return rows > 0 ? launch(padded_copy_kernel, dim3((unsigned)((rows + 3) / 4)), 256, 0, s, a) : hipSuccess;
+    const int64_t groups = (rows + 3) / 4;
+    return rows > 0 ? launch(padded_copy_kernel, dim3((unsigned)(groups < kCopyGroups ? groups : kCopyGroups)), 256, 0, s, a) : hipSuccess;
 }
 
 // ---- weight gradients ----------------------------------------------------------

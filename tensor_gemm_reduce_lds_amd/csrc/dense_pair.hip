@@ -4,10 +4,6 @@
 namespace gemm_rs {
 namespace ffn {
 
-template <TileKind KIND>
-hipError_t launch_dense(DenseArgs &a, bool col, bool direct, int64_t slot_bytes, hipStream_t s) {
-    return col ? launch_dense_form<KIND, true>(a, direct, slot_bytes, s) : launch_dense_form<KIND, false>(a, direct, slot_bytes, s);
-}
 template hipError_t launch_dense<kPair>(DenseArgs &, bool, bool, int64_t, hipStream_t);
 
 }  // namespace ffn

@@ -18,9 +18,8 @@ struct TileAt {
     int64_t m0, n0;
     int32_t m_left;
 };
-// Workgroup b's tile (of a launch of `of` workgroups for each part).  Row tiles in
-// groups of 8, a group column by column, so that the tiles that run together read
-// few rows of A and columns of B.
+// Workgroup b's tile.  Row tiles in groups of 8, a group column by column, so that
+// the tiles that run together read few rows of A and columns of B.
 template <class T>
 __device__ __forceinline__ TileAt tile_at(const DenseArgs &p, uint32_t b) {
     const uint32_t tiles = (uint32_t)p.tiles_m * (uint32_t)p.tiles_n, unit = b / tiles, t = b - unit * tiles;
@@ -444,6 +443,24 @@ hipError_t launch_dense_form(DenseArgs &a, bool direct, int64_t slot_bytes, hipS
     case kDense128Deep: return launch_dense_tile<KIND, false, COL, 128, 128, 2, 4, 4, 4>(a, n, b, s);
     default: return launch_dense_tile<KIND, false, COL, 64, 128, 2, 2, 3, 3>(a, n, b, s);
     }
+}
+
+// All rows, in as many launches as they take.
+template <TileKind KIND>
+hipError_t launch_dense(DenseArgs &all, bool col, bool direct, int64_t slot_bytes, hipStream_t s) {
+    const int64_t most = rows_of_launch(all.N);
+    for (int64_t r = 0; r < all.rows; r += most) {
+        DenseArgs a = all;
+        auto below = [r](const void *p, int64_t ld, int elem) { return p ? (char *)p + r * ld * elem : nullptr; };
+        a.rows = all.rows - r < most ? all.rows - r : most;
+        for (const uint16_t *&A : a.A) A = (const uint16_t *)below(A, a.lda, 2);
+        a.R = below(a.R, a.ldr, a.out_f32 ? 4 : 2);
+        a.D[0] = below(a.D[0], a.ldd, a.out_f32 ? 4 : 2);
+        for (void *&Z : a.Z) Z = below(Z, a.ldz, a.z_f32 ? 4 : 2);
+        const hipError_t e = col ? launch_dense_form<KIND, true>(a, direct, slot_bytes, s) : launch_dense_form<KIND, false>(a, direct, slot_bytes, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace ffn

@@ -289,11 +289,22 @@ __device__ __forceinline__ void quant8(const QuantRow &q, int8_t *row, uint32_t 
     }
 }
 
+// Threads of a launch along one axis.  Workgroups past them are dropped without an
+// error from the runtime, so `launch` refuses such grids.
+constexpr int64_t kMostThreads = UINT32_MAX;
+
+// Rows of a product with N columns whose workgroups fit one launch, for kernels of at
+// most 256 threads to 64 x 64 outputs, with a last tile of up to 256 rows.
+inline int64_t rows_of_launch(int64_t N) {
+    return (kMostThreads / 256 / ((N + 63) / 64) * 64 - 256) / 256 * 256;
+}
+
 // Launches a kernel.  The result is this launch's: the thread's last error may
 // be an older one of the caller's, who may not have asked for it, and stays his.
 template <class... P, class... A>
 inline hipError_t launch(void (*kernel)(P...), dim3 grid, int threads, int lds_bytes, hipStream_t s, const A &...args) {
     static_assert(sizeof...(P) == sizeof...(A), "an argument for each parameter");
+    if ((int64_t)grid.x * threads > kMostThreads) return hipErrorInvalidConfiguration;
     return [&](P... held) {      // the arguments in the parameters' types
         void *at[] = {(void *)&held...};
         return own(hipLaunchKernel((const void *)kernel, grid, dim3((unsigned)threads), at, (size_t)lds_bytes, s));
@@ -316,6 +327,7 @@ inline hipError_t launch_lds(int64_t blocks, int threads, int lds_bytes, hipStre
         if (e != hipSuccess) return e;
         set[dev].store(true, std::memory_order_release);
     }
+    if (blocks > kMostThreads / threads) return hipErrorInvalidConfiguration;
     return launch(KERNEL, dim3((unsigned)blocks), threads, lds_bytes, s, a);
 }
 
