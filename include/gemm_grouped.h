@@ -93,7 +93,8 @@ GEMM_RS_API int gemm_grouped_plan(const gemm_grouped_desc_t *desc, gemm_grouped_
  * may be NULL then, as arrays without elements are.
  * One plan of TN must not run on two streams at once (its workspace).
  * Returns OK, INVALID_ARG (NULL or misaligned pointers, rows out of range,
- * another device) or HIP.
+ * another device) or HIP (also where the workgroups have more threads than one
+ * launch, 2^32: 2^30 rows with the slower kernel).
  */
 GEMM_RS_API int gemm_grouped_run(gemm_grouped_plan_t plan, const void *A, const void *B,
                                  const void *offsets, void *C, int64_t rows, void *stream);

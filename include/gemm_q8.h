@@ -77,7 +77,8 @@ GEMM_RS_API int gemm_q8_plan(const gemm_q8_desc_t *desc, gemm_q8_plan_t *out);
  * With rows == 0 nothing is enqueued, and a, a_scale and D may be NULL, as
  * arrays without elements are.
  * Returns OK, INVALID_ARG (missing, superfluous or misaligned pointers, rows
- * out of range, another device) or HIP.
+ * out of range, another device) or HIP (also for more than about
+ * 2^28 channels, whose workgroups have more threads than one launch).
  */
 GEMM_RS_API int gemm_q8_run(gemm_q8_plan_t plan, const void *a, const void *a_scale,
                             const void *w, const void *w_scale, const void *bias, void *D,

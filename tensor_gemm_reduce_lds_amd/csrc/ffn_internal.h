@@ -294,9 +294,11 @@ __device__ __forceinline__ void quant8(const QuantRow &q, int8_t *row, uint32_t 
 constexpr int64_t kMostThreads = UINT32_MAX;
 
 // Rows of a product with N columns whose workgroups fit one launch, for kernels of at
-// most 256 threads to 64 x 64 outputs, with a last tile of up to 256 rows.
+// most 256 threads to 64 x 64 outputs, with a last tile of up to 256 rows.  (At least
+// a tile: a row of 2^28 columns is refused by `launch`.)
 inline int64_t rows_of_launch(int64_t N) {
-    return (kMostThreads / 256 / ((N + 63) / 64) * 64 - 256) / 256 * 256;
+    const int64_t rows = (kMostThreads / 256 / ((N + 63) / 64) * 64 - 256) / 256 * 256;
+    return rows < 256 ? 256 : rows;
 }
 
 // Launches a kernel.  The result is this launch's: the thread's last error may

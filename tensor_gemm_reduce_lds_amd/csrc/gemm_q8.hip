@@ -273,7 +273,7 @@ hipError_t launch_rows(const Q8Args &q, hipStream_t s) {
     return launch_lds<q8_rows_kernel<MB, NB, NW, S>>((q.N + NB * 16 - 1) / (NB * 16), NW * 64, R::LDS_BYTES, s, q);
 }
 
-hipError_t launch_product(const Q8Args &q, hipStream_t s) {
+hipError_t launch_rows_of(const Q8Args &q, hipStream_t s) {
     switch (q8_choice(q.M, q.N)) {
     case kQ8Rows16: return launch_rows<1, 1, 8, 4>(q, s);
     case kQ8Rows16Wide: return launch_rows<1, 2, 8, 3>(q, s);
@@ -288,6 +288,21 @@ hipError_t launch_product(const Q8Args &q, hipStream_t s) {
     case kQ8Tile64x128Deep: return launch_tile<64, 128, 2, 2, 3, 3>(q, s);
     default: return launch_tile<64, 64, 2, 2, 4, 4>(q, s);
     }
+}
+
+// All rows, in as many launches as they take.
+hipError_t launch_product(const Q8Args &all, hipStream_t s) {
+    const int64_t most = rows_of_launch(all.N);
+    for (int64_t r = 0; r < all.M; r += most) {
+        Q8Args q = all;
+        q.M = all.M - r < most ? all.M - r : most;
+        q.a += r * q.lda;
+        q.a_scale += r;
+        q.D = (char *)q.D + r * q.ldd * (q.out_f32 ? 4 : 2);
+        const hipError_t e = launch_rows_of(q, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 int validate(const gemm_q8_desc_t &d) {
