@@ -94,7 +94,8 @@ GEMM_RS_API int gemm_epi_plan(const gemm_epi_desc_t *desc, gemm_epi_plan_t *out)
  * rows == 0 nothing is enqueued, and arrays of rows may be NULL, as arrays without
  * elements are.  One plan must not run on two streams at once (its workspace).
  * Returns OK, INVALID_ARG (a missing or superfluous pointer, an address not
- * aligned to its element, rows out of range, another device) or HIP.
+ * aligned to its element, rows out of range, another device, an output in place of
+ * an input of another stride or element size) or HIP.
  */
 GEMM_RS_API int gemm_epi_run(gemm_epi_plan_t plan, const void *x, const void *w, const void *bias, const void *r,
                              void *y, void *z, int64_t rows, void *stream);

@@ -135,7 +135,8 @@ GEMM_RS_API int gemm_gated_run(gemm_gated_plan_t plan, const void *x, const void
  * of weights and biases are zeros (with `accumulate` nothing is added), and
  * arrays of rows may be NULL.  But for dz in place of z no output may overlap an
  * input or another output.  One plan must not run on two streams at once (its
- * workspace).
+ * workspace).  Returns as gemm_gated_run, and INVALID_ARG for dz in place of z that
+ * is float or has another stride.
  */
 GEMM_RS_API int gemm_gated_backward(gemm_gated_plan_t plan, const void *dh, const void *x, const void *w_gate,
                                     const void *w_up, const void *z_gate, const void *z_up, void *dz_gate,

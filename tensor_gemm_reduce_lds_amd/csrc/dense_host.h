@@ -14,6 +14,11 @@ namespace ffn {
 constexpr int64_t kDenseMaxRows = INT32_MAX - 1024;
 
 inline bool flag(int32_t v) { return v == 0 || v == 1; }
+// Whether an output may be `in` itself: not where its elements are of another size or
+// its rows lie elsewhere, since others would be overwritten before they are read.
+inline bool in_place_ok(const void *out, const void *in, bool same_size, int64_t rows, int64_t ld_out, int64_t ld_in) {
+    return !out || out != in || (same_size && (ld_out == ld_in || rows <= 1));
+}
 inline bool stride_ok(int64_t ld, int64_t cols) { return ld >= 0 && (ld == 0 || ld >= cols); }
 
 // What both plans are made of.  Strides are filled in; ldd: of dz as an operand.

@@ -71,6 +71,7 @@ int gemm_epi_run(gemm_epi_plan_t p, const void *x, const void *w, const void *bi
         return GEMM_RS_ERR_INVALID_ARG;
     if (!aligned(x, 2) || !aligned(w, 2) || !aligned(bias, type_bytes(d.bias_dtype)) || !aligned(r, oe) || !aligned(y, oe) || !aligned(z, ze))
         return GEMM_RS_ERR_INVALID_ARG;
+    if (!in_place_ok(y, r, true, rows, d.ldy, d.ldr)) return GEMM_RS_ERR_INVALID_ARG;
     if (!some) return GEMM_RS_OK;
     DenseArgs a = {};
     a.bias_f32 = d.bias_dtype == GEMM_RS_F32;
@@ -99,6 +100,7 @@ int gemm_epi_backward(gemm_epi_plan_t p, const void *dy, const void *x, const vo
     if (!aligned(dy, ye) || !aligned(x, 2) || !aligned(w, 2) || !aligned(z, ze) || !aligned(dz, 2) || !aligned(dx, 2) ||
         !aligned(dw, type_bytes(d.dw_dtype)) || !aligned(dbias, 4))
         return GEMM_RS_ERR_INVALID_ARG;
+    if (!in_place_ok(dz, z, ze == 2, rows, d.lddz, d.ldz) || !in_place_ok(dz, dy, !f32, rows, d.lddz, d.lddy)) return GEMM_RS_ERR_INVALID_ARG;
     if (!some && d.accumulate) return GEMM_RS_OK;
     hipStream_t s = (hipStream_t)stream;
     // dz into a padded copy too, where one is needed and has room

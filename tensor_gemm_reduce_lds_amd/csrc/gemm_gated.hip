@@ -97,6 +97,9 @@ int gemm_gated_backward(gemm_gated_plan_t p, const void *dh, const void *x, cons
     for (const void *q : {dh, x, w_gate, w_up, (const void *)dz_gate, (const void *)dz_up, (const void *)dx})
         if (!aligned(q, 2)) return GEMM_RS_ERR_INVALID_ARG;
     if (!aligned(z_gate, ze) || !aligned(z_up, ze) || !aligned(dw_gate, we) || !aligned(dw_up, we) || !aligned(db_gate, 4) || !aligned(db_up, 4)) return GEMM_RS_ERR_INVALID_ARG;
+    for (const void *out : {dz_gate, dz_up})
+        for (const void *in : {z_gate, z_up})
+            if (!in_place_ok(out, in, ze == 2, rows, d.lddz, d.ldz)) return GEMM_RS_ERR_INVALID_ARG;
     if (!some && d.accumulate) return GEMM_RS_OK;
     hipStream_t s = (hipStream_t)stream;
     // dz into a padded copy too, where one is needed and has room

@@ -74,3 +74,29 @@ def test_epi(out):
         back(dy, x, w, z, dz, dx, dw, db)
         torch.cuda.synchronize()
         assert all(bool((o != 7.0).any()) for o in outs)
+
+
+def test_in_place_of_another_stride_or_size():
+    """y over r, dz over z or dy: threads would overwrite what others read."""
+    lib, bad, ok = F._library(), G.ERR_INVALID_ARG, G.OK
+    t = torch.zeros(1 << 16, device="cuda")
+    a = [t.data_ptr() + 4096 * k for k in range(16)]
+    for strides, same in ((dict(), True), (dict(ldr=40, ldy=32, ldz=40, lddz=32, lddy=40), False)):
+        with F.EpiPlan(8, 32, 16, act=F.ACT_GELU, has_residual=1, backward=1, **strides) as plan:
+            for rows in (0, 1, 8):
+                want = ok if same or rows < 2 else bad
+                assert lib.gemm_epi_run(plan.handle, a[0], a[1], None, a[2], a[2], a[3], rows, None) == want
+                for dz in (a[4], a[5]):                # dy, z
+                    assert lib.gemm_epi_backward(plan.handle, a[4], a[0], a[1], a[5], dz, a[6], a[7], None, rows, None) == want
+                assert lib.gemm_epi_backward(plan.handle, a[4], a[0], a[1], a[5], a[8], a[6], a[7], None, rows, None) == ok
+        strides = {k: v for k, v in strides.items() if k in ("ldz", "lddz")}
+        with F.GatedPlan(8, 32, 16, backward=1, **strides) as plan:
+            for rows in (0, 1, 8):
+                want = ok if same or rows < 2 else bad
+                for dz in ((a[5], a[6]), (a[5], a[7]), (a[7], a[6])):
+                    assert lib.gemm_gated_backward(plan.handle, a[4], a[0], a[1], a[2], a[5], a[6], *dz, a[8], a[9], a[10], None, None, rows, None) == want
+    with F.EpiPlan(8, 32, 16, act=F.ACT_GELU, out_dtype=F.F32, backward=1, z_dtype=F.F32) as plan, F.GatedPlan(8, 32, 16, backward=1, z_dtype=F.F32) as gated:
+        for dz in (a[4], a[5]):
+            assert lib.gemm_epi_backward(plan.handle, a[4], a[0], a[1], a[5], dz, a[6], a[7], None, 1, None) == bad
+        assert lib.gemm_gated_backward(gated.handle, a[4], a[0], a[1], a[2], a[5], a[6], a[5], a[6], a[8], a[9], a[10], None, None, 1, None) == bad
+    torch.cuda.synchronize()
