@@ -69,7 +69,11 @@ __device__ __forceinline__ void sum_parts(const DenseArgs &p, const TileAt &t, i
 // What finishes a tile's values as a thread gets them.  RES: residuals are fetched
 // ahead, those of all stripes at once, but of floats, for which few registers are left,
 // of two, and each of the others when its place is free (8192 x 8192 x 3584 in floats
-// with bias and residual 512 us; a stripe at a time 524, of three 549).
+// with bias and residual 512 us; a stripe at a time 524, of three 549).  Beside the 128
+// accumulators of a 256 x 256 tile's thread they leave too few registers in the
+// epilogue, which spills 19 to 21 of them (48 and 56 bytes of scratch a lane), and 49
+// (92 bytes) in the weight gradients, where all forms of output, added to or not, are
+// one kernel; the loop over the contraction spills none.
 template <class T, bool F32, bool STREAM, bool RES>
 struct FinishOne {
     static constexpr auto ORDER = F32 ? T::kSplit : T::kRun8;
